@@ -56,6 +56,8 @@ enum { MOE_F32 = 0, MOE_BF16 = 1 };
  *                 stacked on dim 0, gate then up concatenated on dim 1):
  *                 E(x) = W_down (silu(W_gate x) * (W_up x)). No biases. */
 enum { MOE_ACT_GELU = 0, MOE_ACT_SWIGLU = 1 };
+/* No activation: for moe_ckpt and moe_q4 only, not an expert FFN kind. */
+enum { MOE_ACT_NONE = 2 };
 
 /* Return codes. */
 enum {
@@ -369,6 +371,136 @@ size_t moe_backward_workspace_size(const moe_config *cfg, int64_t T);
 int moe_backward(const moe_config *cfg, const void *x, int64_t T, const moe_weights *w, const float *dy,
                  float alpha_switch, float alpha_importance, moe_grads *grads, void *ws, size_t ws_bytes,
                  moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Expert operators beside the layer call: the products, the activation's
+ * checkpoint and backward pass, and 4-bit weights, on rows that are already
+ * grouped (by moe_ep_dispatch, a workspace's tables, or the caller).  They
+ * follow the conventions above: caller-owned device memory, work enqueued on
+ * `stream`, nothing allocated or kept, arguments checked on the host before
+ * anything is enqueued.  None needs a workspace, so calls may overlap on
+ * several streams and be captured into graphs freely; outputs must not
+ * overlap inputs.  Results are bitwise reproducible.  The buffers and the
+ * stream belong to the current device.
+ * ------------------------------------------------------------------------ */
+
+/* Matrix products grouped by expert over ragged row segments (Transformers-v5
+ * MoE article, section 2, the grouped_mm backend: one product per expert over
+ * the rows routed to it).  The rows of group g are row_offsets[g] ..
+ * row_offsets[g + 1] - 1 of the row operands, any lengths, zero included;
+ * weights are stored out x in, n x k per group.
+ *   MOE_GMM_NT  c[r, 0..n) = sum_i a[r, i] b[g, :, i]   an expert's linear:
+ *               a [rows, k], b [groups, n, k], c [rows, n]
+ *   MOE_GMM_NN  c[r, 0..k) = sum_i a[r, i] b[g, i, :]   its input's gradient:
+ *               a [rows, n], b [groups, n, k], c [rows, k]
+ *   MOE_GMM_TN  c[g] = sum over the group's rows a[r, :]^T b[r, :]   its
+ *               weight's gradient: a [rows, n], b [rows, k], c [groups, n, k];
+ *               zero for a group without rows
+ * bf16 operands give bf16 or fp32 results, fp32 operands fp32 ones; sums are
+ * held in fp32 and rounded once at the end. */
+enum { MOE_GMM_NT = 0, MOE_GMM_NN = 1, MOE_GMM_TN = 2 };
+typedef struct {
+    int32_t kind;       /* MOE_GMM_* */
+    int32_t groups;     /* 1..1024 */
+    int32_t n, k;       /* multiples of 8 (bf16) or 4 (fp32) */
+    int32_t dtype;      /* of a and b: MOE_F32 or MOE_BF16 */
+    int32_t out_dtype;  /* of c */
+    int32_t accumulate; /* MOE_GMM_TN only: 1 adds to c (gradients of several
+                           batches; the sum is formed in fp32, then rounded to
+                           out_dtype), 0 overwrites it */
+    int32_t reserved;   /* 0 */
+    int64_t lda, ldb, ldc; /* row strides in elements, 0 = contiguous; a
+                           multiple of 16 bytes.  A group's weights (b, or c of
+                           MOE_GMM_TN) are n such rows and follow each other. */
+} moe_gmm;
+/* row_offsets [groups + 1] int32 (device), non-decreasing, within 0..rows;
+ * rows: the rows that a (MOE_GMM_TN: a and b) holds.  Rows outside every
+ * segment are not used and rows of c there are left as they were.  Offsets
+ * that break the rule are clamped to it and set MOE_STATUS_BOUNDS. */
+int moe_grouped_mm(const moe_gmm *d, const void *a, const void *b, void *c, const int32_t *row_offsets,
+                   int64_t rows, moe_stream_t stream);
+
+/* Activation checkpoints in 8 bits and their use in the backward pass: the
+ * experts' pre-activations u are kept as one byte per value and one scale per
+ * group of values, and the activation is recomputed from them.
+ * For each group of `group` consecutive values of a row (for MOE_ACT_SWIGLU of
+ * its gate half and of its up half; the last group of a half may be short)
+ *   e = the smallest integer >= -126 with max|u| <= L 2^e,  L = 127 or 448
+ *       (at most 121 or 119: magnitudes above L 2^e then saturate, so that u^
+ *       stays finite),
+ *   q = u 2^-e rounded to nearest even, as an int8 or an e4m3 value,
+ * and the scale byte is e + 127; the checkpoint stands for u^ = q 2^e.  A group
+ * that holds an infinity or a NaN gets the scale byte 255 and stands for NaN.
+ *   u  [rows, C] dtype, C = 2 width (MOE_ACT_SWIGLU: gate, then up) or width
+ *   q  [rows, C] uint8, scales [rows, (C / width) * ceil(width / group)] uint8,
+ *   both contiguous. */
+enum { MOE_CKPT_INT8 = 0, MOE_CKPT_E4M3 = 1 };
+typedef struct {
+    int32_t width;  /* a multiple of 8 (bf16) or 4 (fp32) */
+    int32_t act;    /* MOE_ACT_GELU, MOE_ACT_SWIGLU, or MOE_ACT_NONE: rows are
+                       saved and loaded as they are (an expert's input) */
+    int32_t dtype;  /* of u, h, dh, du and hw */
+    int32_t format; /* MOE_CKPT_* */
+    int32_t group;  /* 32, 64 or 128 */
+    int32_t reserved; /* 0 */
+    int64_t ldu, ldh; /* row strides in elements of u and du, and of h, dh and
+                       hw; 0 = contiguous; a multiple of 16 bytes */
+} moe_ckpt;
+/* h [rows, width] = act(u), from u itself and rounded once, and u's
+ * checkpoint.  With MOE_ACT_NONE h is not written and may be NULL. */
+int moe_ckpt_forward(const moe_ckpt *d, const void *u, int64_t rows, void *h, uint8_t *q, uint8_t *scales,
+                     moe_stream_t stream);
+/* u [rows, C] = the values the checkpoint stands for (exact in fp32; in bf16
+ * exact too but for subnormals). */
+int moe_ckpt_load(const moe_ckpt *d, const uint8_t *q, const uint8_t *scales, int64_t rows, void *u,
+                  moe_stream_t stream);
+/* The activation's backward pass from the checkpoint, for rows that enter the
+ * layer's output with the gate weight w[r] (fp32 [rows], NULL: 1):
+ *   dh [rows, width]  the gradient of the unweighted rows' h (W2^T dy)
+ *   du [rows, C] = w dh act'(u^)            hw [rows, width] = w act(u^), or NULL
+ *   dw [rows] fp32 = sum_i dh_i act(u^)_i, the gate weight's gradient, or NULL
+ * MOE_ACT_NONE has no backward pass (MOE_ERR_INVALID_ARG). */
+int moe_ckpt_backward(const moe_ckpt *d, const uint8_t *q, const uint8_t *scales, int64_t rows, const void *dh,
+                      const float *w, void *du, void *hw, float *dw, moe_stream_t stream);
+
+/* Products of single rows with 4-bit expert weights (decode): W [experts, n, k]
+ * out x in is held as codes [experts, n, k / 2] uint8, value 2j of a row in
+ * the low four bits of its byte j and value 2j + 1 in the high ones, and scales
+ * [experts, n, ceil(k / group)] for groups of consecutive values of a row:
+ *   MOE_Q4_INT4  (code - 8) * scale, bf16 scales, groups of 32, 64 or 128
+ *   MOE_Q4_E2M1  0, .5, 1, 1.5, 2, 3, 4, 6 by the low three bits, the fourth
+ *                is the sign, times 2^(scale - 127), uint8 scales (255: NaN),
+ *                groups of 32 */
+enum { MOE_Q4_INT4 = 0, MOE_Q4_E2M1 = 1 };
+typedef struct {
+    int32_t experts; /* 1..1024 */
+    int32_t n;       /* rows of an expert's matrix: a multiple of 8 (SwiGLU: 16) */
+    int32_t k;       /* a multiple of 32 */
+    int32_t group;   /* values per scale */
+    int32_t format;  /* MOE_Q4_* */
+    int32_t act;     /* applied to the products: MOE_ACT_NONE, MOE_ACT_GELU, or
+                        MOE_ACT_SWIGLU (rows 0..n/2-1 gate, n/2..n-1 up) */
+} moe_q4;
+/* codes and scales of W [experts, n, k] in w_dtype.  int4: scale = max|w| / 7
+ * rounded to bf16, code = 8 + w / scale rounded to nearest even; e2m1: the
+ * smallest power of two with max|w| <= 6 scale, nearest value, ties to the even
+ * code.  A group with an infinity or a NaN gets a NaN scale. */
+int moe_q4_quantize(const moe_q4 *d, const void *W, int32_t w_dtype, uint8_t *codes, void *scales,
+                    moe_stream_t stream);
+/* W [experts, n, k] in w_dtype: the values, rounded once (for moe_grouped_mm
+ * and moe_forward on long prompts). */
+int moe_q4_dequantize(const moe_q4 *d, const uint8_t *codes, const void *scales, void *W, int32_t w_dtype,
+                      moe_stream_t stream);
+/* For pair p = 0..pairs-1 (pairs <= 4096) with expert e = expert[p]:
+ *   y[p] = gate[p] * act(W[e] x[p / x_div]),  fp32 sums, rounded once
+ *   x [ceil(pairs / x_div), k] bf16: x_div = TopK reads each token's row for
+ *     its slots (moe_route's topk_idx is expert then), 1 a row per pair
+ *   gate [pairs] fp32 or NULL (1); y [pairs, n or n / 2 (SwiGLU)] in y_dtype
+ * A pair with expert -1 (a dropped assignment) gets a row of zeros; so does one
+ * with another index out of range, which also sets MOE_STATUS_BOUNDS. */
+int moe_q4_matvec(const moe_q4 *d, const void *x, int64_t pairs, int32_t x_div, const int32_t *expert,
+                  const uint8_t *codes, const void *scales, const float *gate, void *y, int32_t y_dtype,
+                  moe_stream_t stream);
 
 /* Where moe_forward leaves its intermediates inside the workspace (byte
  * offsets from ws), for inspection in tests.  Rows of each expert's segment in

@@ -22,8 +22,11 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoe_debug.so" if os.environ.get("MOE_BOUNDS_CHECK") == "1" else "libmoe.so")
 
 MOE_F32, MOE_BF16 = 0, 1
-MOE_ACT_GELU, MOE_ACT_SWIGLU = 0, 1
+MOE_ACT_GELU, MOE_ACT_SWIGLU, MOE_ACT_NONE = 0, 1, 2
 MOE_OVERFLOW_DROP, MOE_OVERFLOW_REROUTE = 0, 1
+MOE_GMM_NT, MOE_GMM_NN, MOE_GMM_TN = 0, 1, 2
+MOE_CKPT_INT8, MOE_CKPT_E4M3 = 0, 1
+MOE_Q4_INT4, MOE_Q4_E2M1 = 0, 1
 MOE_N_STAGES = 7
 STAGE_NAMES = ("route", "scan", "permute", "up", "down", "combine", "stats")
 
@@ -40,7 +43,8 @@ MOE_NOALLOC_SCRATCH_BYTES = 2 << 20
 EXPORTED = ("moe_workspace_size", "moe_route", "moe_forward", "moe_forward_timed", "moe_aux_stats",
             "moe_aux_stats_noalloc", "moe_aux_partials", "moe_aux_finalize", "moe_aux_finalize_host",
             "moe_ep_workspace_size", "moe_ep_dispatch", "moe_ep_experts_workspace_size", "moe_ep_experts",
-            "moe_ep_combine", "moe_backward_workspace_size", "moe_backward",
+            "moe_ep_combine", "moe_backward_workspace_size", "moe_backward", "moe_grouped_mm", "moe_ckpt_forward",
+            "moe_ckpt_load", "moe_ckpt_backward", "moe_q4_quantize", "moe_q4_dequantize", "moe_q4_matvec",
             "moe_get_workspace_layout", "moe_total_params", "moe_active_params", "moe_get_device_status",
             "moe_launch_count", "moe_error_string", "moe_selftest_wait_timeout")
 
@@ -67,6 +71,24 @@ class moe_aux(ctypes.Structure):
 class moe_grads(ctypes.Structure):
     _fields_ = [("dx", ctypes.c_void_p), ("dW_g", ctypes.c_void_p), ("db_g", ctypes.c_void_p),
                 ("dW1", ctypes.c_void_p), ("db1", ctypes.c_void_p), ("dW2", ctypes.c_void_p), ("db2", ctypes.c_void_p)]
+
+
+class moe_gmm(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("groups", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64),
+                ("ldc", ctypes.c_int64)]
+
+
+class moe_ckpt(ctypes.Structure):
+    _fields_ = [("width", ctypes.c_int32), ("act", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("format", ctypes.c_int32), ("group", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("ldu", ctypes.c_int64), ("ldh", ctypes.c_int64)]
+
+
+class moe_q4(ctypes.Structure):
+    _fields_ = [("experts", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("format", ctypes.c_int32), ("act", ctypes.c_int32)]
 
 
 class moe_workspace_layout(ctypes.Structure):
@@ -131,6 +153,21 @@ def load_library():
     L.moe_backward.restype = ctypes.c_int
     L.moe_backward.argtypes = [cfgp, vp, i64, wp, vp, ctypes.c_float, ctypes.c_float, ctypes.POINTER(moe_grads), vp,
                                sz, vp]
+    gmmp, ckp, q4p = ctypes.POINTER(moe_gmm), ctypes.POINTER(moe_ckpt), ctypes.POINTER(moe_q4)
+    L.moe_grouped_mm.restype = ctypes.c_int
+    L.moe_grouped_mm.argtypes = [gmmp, vp, vp, vp, vp, i64, vp]
+    L.moe_ckpt_forward.restype = ctypes.c_int
+    L.moe_ckpt_forward.argtypes = [ckp, vp, i64, vp, vp, vp, vp]
+    L.moe_ckpt_load.restype = ctypes.c_int
+    L.moe_ckpt_load.argtypes = [ckp, vp, vp, i64, vp, vp]
+    L.moe_ckpt_backward.restype = ctypes.c_int
+    L.moe_ckpt_backward.argtypes = [ckp, vp, vp, i64, vp, vp, vp, vp, vp, vp]
+    L.moe_q4_quantize.restype = ctypes.c_int
+    L.moe_q4_quantize.argtypes = [q4p, vp, i32, vp, vp, vp]
+    L.moe_q4_dequantize.restype = ctypes.c_int
+    L.moe_q4_dequantize.argtypes = [q4p, vp, vp, vp, i32, vp]
+    L.moe_q4_matvec.restype = ctypes.c_int
+    L.moe_q4_matvec.argtypes = [q4p, vp, i64, i32, vp, vp, vp, vp, vp, i32, vp]
     L.moe_get_workspace_layout.restype = ctypes.c_int
     L.moe_get_workspace_layout.argtypes = [cfgp, i64, ctypes.POINTER(moe_workspace_layout)]
     L.moe_total_params.restype = i64
@@ -303,6 +340,53 @@ def moe_backward(cfg, x, T, weights, dy, alpha_switch, alpha_importance, grads, 
     return load_library().moe_backward(ctypes.byref(cfg), _ptr(x), T, ctypes.byref(weights), _ptr(dy),
                                        float(alpha_switch), float(alpha_importance), ctypes.byref(grads), _ptr(ws),
                                        ws_bytes, _stream(stream))
+
+
+def make_gmm(kind, groups, n, k, dtype=MOE_BF16, out_dtype=MOE_BF16, accumulate=False, lda=0, ldb=0, ldc=0) -> moe_gmm:
+    return moe_gmm(kind, groups, n, k, dtype, out_dtype, int(bool(accumulate)), 0, lda, ldb, ldc)
+
+
+def moe_grouped_mm(d, a, b, c, row_offsets, rows, stream=None) -> int:
+    """Products grouped by expert; row_offsets: device int32 [groups + 1]."""
+    return load_library().moe_grouped_mm(ctypes.byref(d), _ptr(a), _ptr(b), _ptr(c), _ptr(row_offsets), rows,
+                                         _stream(stream))
+
+
+def make_ckpt(width, act=MOE_ACT_SWIGLU, dtype=MOE_BF16, format=MOE_CKPT_INT8, group=128, ldu=0, ldh=0) -> moe_ckpt:
+    return moe_ckpt(width, act, dtype, format, group, 0, ldu, ldh)
+
+
+def moe_ckpt_forward(d, u, rows, h, q, scales, stream=None) -> int:
+    return load_library().moe_ckpt_forward(ctypes.byref(d), _ptr(u), rows, _ptr(h), _ptr(q), _ptr(scales),
+                                           _stream(stream))
+
+
+def moe_ckpt_load(d, q, scales, rows, u, stream=None) -> int:
+    return load_library().moe_ckpt_load(ctypes.byref(d), _ptr(q), _ptr(scales), rows, _ptr(u), _stream(stream))
+
+
+def moe_ckpt_backward(d, q, scales, rows, dh, w, du, hw, dw, stream=None) -> int:
+    return load_library().moe_ckpt_backward(ctypes.byref(d), _ptr(q), _ptr(scales), rows, _ptr(dh), _ptr(w), _ptr(du),
+                                            _ptr(hw), _ptr(dw), _stream(stream))
+
+
+def make_q4(experts, n, k, group, format=MOE_Q4_INT4, act=MOE_ACT_NONE) -> moe_q4:
+    return moe_q4(experts, n, k, group, format, act)
+
+
+def moe_q4_quantize(d, W, w_dtype, codes, scales, stream=None) -> int:
+    return load_library().moe_q4_quantize(ctypes.byref(d), _ptr(W), w_dtype, _ptr(codes), _ptr(scales),
+                                          _stream(stream))
+
+
+def moe_q4_dequantize(d, codes, scales, W, w_dtype, stream=None) -> int:
+    return load_library().moe_q4_dequantize(ctypes.byref(d), _ptr(codes), _ptr(scales), _ptr(W), w_dtype,
+                                            _stream(stream))
+
+
+def moe_q4_matvec(d, x, pairs, x_div, expert, codes, scales, gate, y, y_dtype, stream=None) -> int:
+    return load_library().moe_q4_matvec(ctypes.byref(d), _ptr(x), pairs, x_div, _ptr(expert), _ptr(codes),
+                                        _ptr(scales), _ptr(gate), _ptr(y), y_dtype, _stream(stream))
 
 
 def moe_get_workspace_layout(cfg, T) -> moe_workspace_layout:

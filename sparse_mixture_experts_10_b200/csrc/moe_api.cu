@@ -13,11 +13,14 @@
 // excepted, which synchronises the device).
 #include "../../include/moe.h"
 #include "moe_backward.cuh"
+#include "moe_ckpt.cuh"
 #include "moe_common.cuh"
 #include "moe_decode_fused.cuh"
 #include "moe_gemm_simt.cuh"
 #include "moe_gemm_decode.cuh"
 #include "moe_gemm_tc.cuh"
+#include "moe_grouped_mm.cuh"
+#include "moe_q4.cuh"
 #include "moe_route.cuh"
 #include "moe_router_tc.cuh"
 
@@ -2017,3 +2020,5 @@ int moe_selftest_wait_timeout(int64_t timeout_ns, moe_stream_t stream) {
 }
 
 }  // extern "C"
+
+#include "moe_expert_ops.cuh"

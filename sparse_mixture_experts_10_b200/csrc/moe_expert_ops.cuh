@@ -1,0 +1,319 @@
+// moe_expert_ops.cuh -- host side of the expert operators beside the layer
+// call: grouped products, 8-bit activation checkpoints, 4-bit expert products.
+// Included by moe_api.cu after its helpers; argument checks come before any
+// launch, nothing is allocated and no stream is synchronised.
+#pragma once
+
+namespace {
+
+bool aligned4(const void *ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3u) == 0; }
+bool dtype_ok(int32_t d) { return d == MOE_F32 || d == MOE_BF16; }
+int64_t elem_size(int32_t d) { return d == MOE_F32 ? 4 : 2; }
+
+// Row strides: 0 stands for a contiguous row; otherwise at least the row's
+// length and a multiple of 16 bytes.
+int take_stride(int64_t given, int64_t cols, int64_t es, int64_t *out) {
+    *out = given == 0 ? cols : given;
+    if (*out < cols || *out > (int64_t(1) << 32) || (*out * es) % 16 != 0) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+// ---------------------------------------------------------------- grouped products
+struct GmmPlan {
+    gmm::Params p;
+    int64_t a_cols, c_cols;
+};
+
+int make_gmm_plan(const moe_gmm *d, int64_t rows, GmmPlan *out) {
+    if (!d || rows < 0 || rows > INT32_MAX - 1024) return MOE_ERR_INVALID_ARG;
+    if (d->kind != MOE_GMM_NT && d->kind != MOE_GMM_NN && d->kind != MOE_GMM_TN) return MOE_ERR_INVALID_ARG;
+    if (d->groups < 1 || d->groups > gmm::kMaxGroups || d->n < 1 || d->k < 1) return MOE_ERR_INVALID_ARG;
+    if (!dtype_ok(d->dtype) || !dtype_ok(d->out_dtype)) return MOE_ERR_INVALID_ARG;
+    if (d->dtype == MOE_F32 && d->out_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+    if (d->accumulate != 0 && d->accumulate != 1) return MOE_ERR_INVALID_ARG;
+    if (d->accumulate && d->kind != MOE_GMM_TN) return MOE_ERR_UNSUPPORTED;
+    if (d->reserved != 0) return MOE_ERR_INVALID_ARG;
+    const int64_t es = elem_size(d->dtype), os = elem_size(d->out_dtype);
+    if (d->n % (16 / es) || d->k % (16 / es)) return MOE_ERR_INVALID_ARG;
+    gmm::Params &p = out->p;
+    p = gmm::Params{};
+    const bool tn = d->kind == MOE_GMM_TN;
+    out->a_cols = d->kind == MOE_GMM_NT ? d->k : d->n;
+    out->c_cols = d->kind == MOE_GMM_NT ? d->n : d->k;
+    MOE_TRY(take_stride(d->lda, out->a_cols, es, &p.lda));
+    MOE_TRY(take_stride(d->ldb, d->k, es, &p.ldb));
+    MOE_TRY(take_stride(d->ldc, out->c_cols, os, &p.ldc));
+    if (!tn && (double)d->groups * d->n * (double)p.ldb > 4e18) return MOE_ERR_INVALID_ARG;
+    p.rows = rows;
+    p.G = d->groups;
+    p.n = d->n;
+    p.k = d->k;
+    p.accumulate = d->accumulate;
+    p.timeout_ns = kTimeoutNs;
+    return MOE_OK;
+}
+
+template <typename T, typename TO, int KIND>
+int launch_gmm_simt(gmm::Params p, const DeviceInfo &dev, cudaStream_t s) {
+    const int64_t cols = KIND == gmm::NT ? p.n : p.k;
+    p.n_tiles = (int)cdiv(cols, gmm::kTile);
+    int64_t upper;
+    if (KIND == gmm::TN) {
+        p.m_tiles = (int)cdiv(p.n, gmm::kTile);
+        upper = (int64_t)p.G * p.m_tiles * p.n_tiles;
+    } else {
+        upper = (cdiv(p.rows, gmm::kTile) + std::min<int64_t>(p.G, p.rows)) * p.n_tiles;
+    }
+    if (upper > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    p.total = (int)upper;
+    const unsigned grid = (unsigned)std::min<int64_t>(upper, (int64_t)dev.sms * 6);
+    return launch_pdl(gmm::simt_kernel<T, TO, KIND>, dim3(grid), dim3(256), 0, s, p);
+}
+
+template <int KIND>
+int launch_gmm(const moe_gmm *d, const gmm::Params &p, const DeviceInfo &dev, cudaStream_t s) {
+    if (d->dtype == MOE_F32) return launch_gmm_simt<float, float, KIND>(p, dev, s);
+    if (d->out_dtype == MOE_F32) return launch_gmm_simt<__nv_bfloat16, float, KIND>(p, dev, s);
+    return launch_gmm_simt<__nv_bfloat16, __nv_bfloat16, KIND>(p, dev, s);
+}
+
+// ---------------------------------------------------------------- 8-bit checkpoints
+int make_ckpt_params(const moe_ckpt *d, int64_t rows, ckpt::Params *p) {
+    if (!d || rows < 0 || rows > INT32_MAX) return MOE_ERR_INVALID_ARG;
+    if (d->act != MOE_ACT_GELU && d->act != MOE_ACT_SWIGLU && d->act != MOE_ACT_NONE) return MOE_ERR_INVALID_ARG;
+    if (!dtype_ok(d->dtype) || (d->format != MOE_CKPT_INT8 && d->format != MOE_CKPT_E4M3)) return MOE_ERR_INVALID_ARG;
+    if (d->group != 32 && d->group != 64 && d->group != 128) return MOE_ERR_INVALID_ARG;
+    if (d->reserved != 0) return MOE_ERR_INVALID_ARG;
+    const int64_t es = elem_size(d->dtype);
+    if (d->width < 1 || d->width % (16 / es) || d->width > (1 << 28)) return MOE_ERR_INVALID_ARG;
+    *p = ckpt::Params{};
+    MOE_TRY(take_stride(d->ldu, (d->act == MOE_ACT_SWIGLU ? 2 : 1) * (int64_t)d->width, es, &p->ldu));
+    MOE_TRY(take_stride(d->ldh, d->width, es, &p->ldh));
+    p->rows = rows;
+    p->width = d->width;
+    p->group_shift = d->group == 32 ? 5 : d->group == 64 ? 6 : 7;
+    p->sgroups = (int)cdiv(d->width, d->group);
+    // warps of a block that share a row: as many as the row has 512-byte pieces, at most all of them
+    const int64_t pieces = cdiv((int64_t)d->width * es, 512);
+    p->row_warps = 1;
+    while (p->row_warps < ckpt::kThreads / 32 && p->row_warps < pieces) p->row_warps *= 2;
+    return MOE_OK;
+}
+
+dim3 ckpt_grid(const ckpt::Params &p) {
+    return dim3((unsigned)cdiv(p.rows, (ckpt::kThreads / 32) / p.row_warps));
+}
+
+template <typename T, int FMT>
+int launch_ckpt_forward(int act, const ckpt::Params &p, cudaStream_t s) {
+    auto *k = act == MOE_ACT_GELU     ? ckpt::forward_kernel<T, ckpt::GELU, FMT>
+              : act == MOE_ACT_SWIGLU ? ckpt::forward_kernel<T, ckpt::SWIGLU, FMT>
+                                      : ckpt::forward_kernel<T, ckpt::NONE, FMT>;
+    return launch_pdl(k, ckpt_grid(p), dim3(ckpt::kThreads), 0, s, p);
+}
+template <typename T, int FMT>
+int launch_ckpt_backward(int act, const ckpt::Params &p, cudaStream_t s) {
+    auto *k = act == MOE_ACT_GELU ? ckpt::backward_kernel<T, ckpt::GELU, FMT>
+                                  : ckpt::backward_kernel<T, ckpt::SWIGLU, FMT>;
+    return launch_pdl(k, ckpt_grid(p), dim3(ckpt::kThreads), 0, s, p);
+}
+
+// ---------------------------------------------------------------- 4-bit weights
+int make_q4_params(const moe_q4 *d, q4::Params *p) {
+    if (!d || d->experts < 1 || d->experts > 1024) return MOE_ERR_INVALID_ARG;
+    if (d->format != MOE_Q4_INT4 && d->format != MOE_Q4_E2M1) return MOE_ERR_INVALID_ARG;
+    if (d->act != MOE_ACT_GELU && d->act != MOE_ACT_SWIGLU && d->act != MOE_ACT_NONE) return MOE_ERR_INVALID_ARG;
+    if (d->group != 32 && d->group != 64 && d->group != 128) return MOE_ERR_INVALID_ARG;
+    if (d->format == MOE_Q4_E2M1 && d->group != 32) return MOE_ERR_UNSUPPORTED;
+    if (d->n < 1 || d->n % 8 || (d->act == MOE_ACT_SWIGLU && d->n % 16)) return MOE_ERR_INVALID_ARG;
+    if (d->k < 1 || d->k % 32 || d->n > (1 << 20) || d->k > (1 << 20)) return MOE_ERR_INVALID_ARG;
+    *p = q4::Params{};
+    p->N = d->experts;
+    p->n = d->n;
+    p->k = d->k;
+    p->group_shift = d->group == 32 ? 5 : d->group == 64 ? 6 : 7;
+    p->groups = (int)cdiv(d->k, d->group);
+    return MOE_OK;
+}
+
+template <int FMT, int ACT>
+int launch_q4(const q4::Params &p, int y_dtype, cudaStream_t s) {
+    const int cols = ACT == q4::SWIGLU ? p.n / 2 : p.n;
+    const dim3 grid((unsigned)cdiv(cols, q4::kThreads / 32), (unsigned)std::min<int64_t>(p.pairs, 65535));
+    if (y_dtype == MOE_F32) return launch_pdl(q4::matvec_kernel<FMT, ACT, float>, grid, dim3(q4::kThreads), 0, s, p);
+    return launch_pdl(q4::matvec_kernel<FMT, ACT, __nv_bfloat16>, grid, dim3(q4::kThreads), 0, s, p);
+}
+template <int FMT>
+int launch_q4_act(int act, const q4::Params &p, int y_dtype, cudaStream_t s) {
+    if (act == MOE_ACT_GELU) return launch_q4<FMT, q4::GELU>(p, y_dtype, s);
+    if (act == MOE_ACT_SWIGLU) return launch_q4<FMT, q4::SWIGLU>(p, y_dtype, s);
+    return launch_q4<FMT, q4::NONE>(p, y_dtype, s);
+}
+
+constexpr int64_t kQ4MaxPairs = 4096;
+
+}  // namespace
+
+extern "C" {
+
+int moe_grouped_mm(const moe_gmm *d, const void *a, const void *b, void *c, const int32_t *row_offsets, int64_t rows,
+                   moe_stream_t stream) {
+    GmmPlan P;
+    MOE_TRY(make_gmm_plan(d, rows, &P));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool tn = d->kind == MOE_GMM_TN;
+    if (rows == 0) {   // no segment has a row: the weight gradients are zero, the others have nothing to write
+        if (!tn || d->accumulate) return MOE_OK;
+        if (!c || !aligned16(c)) return MOE_ERR_INVALID_ARG;
+        const size_t os = (size_t)elem_size(d->out_dtype);
+        return cudaMemset2DAsync(c, (size_t)P.p.ldc * os, 0, (size_t)d->k * os, (size_t)d->groups * d->n, s) ==
+                       cudaSuccess
+                   ? MOE_OK
+                   : MOE_ERR_CUDA;
+    }
+    if (!a || !b || !c || !row_offsets) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(a) || !aligned16(b) || !aligned16(c) || !aligned4(row_offsets)) return MOE_ERR_INVALID_ARG;
+    DeviceInfo *dev = nullptr;
+    MOE_TRY(device_info(&dev));
+    P.p.A = a;
+    P.p.B = b;
+    P.p.C = c;
+    P.p.row_offsets = row_offsets;
+    if (tn) return launch_gmm<gmm::TN>(d, P.p, *dev, s);
+    if (d->kind == MOE_GMM_NT) return launch_gmm<gmm::NT>(d, P.p, *dev, s);
+    return launch_gmm<gmm::NN>(d, P.p, *dev, s);
+}
+
+int moe_ckpt_forward(const moe_ckpt *d, const void *u, int64_t rows, void *h, uint8_t *q, uint8_t *scales,
+                     moe_stream_t stream) {
+    ckpt::Params p;
+    MOE_TRY(make_ckpt_params(d, rows, &p));
+    if (rows == 0) return MOE_OK;
+    if (!u || !q || !scales || (!h && d->act != MOE_ACT_NONE)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(u) || !aligned16(q) || !aligned16(h)) return MOE_ERR_INVALID_ARG;
+    p.u = u;
+    p.h = h;
+    p.q = q;
+    p.s = scales;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (d->dtype == MOE_F32)
+        return d->format == MOE_CKPT_INT8 ? launch_ckpt_forward<float, ckpt::INT8>(d->act, p, s)
+                                          : launch_ckpt_forward<float, ckpt::E4M3>(d->act, p, s);
+    return d->format == MOE_CKPT_INT8 ? launch_ckpt_forward<__nv_bfloat16, ckpt::INT8>(d->act, p, s)
+                                      : launch_ckpt_forward<__nv_bfloat16, ckpt::E4M3>(d->act, p, s);
+}
+
+int moe_ckpt_load(const moe_ckpt *d, const uint8_t *q, const uint8_t *scales, int64_t rows, void *u,
+                  moe_stream_t stream) {
+    ckpt::Params p;
+    MOE_TRY(make_ckpt_params(d, rows, &p));
+    if (rows == 0) return MOE_OK;
+    if (!u || !q || !scales || !aligned16(u) || !aligned16(q)) return MOE_ERR_INVALID_ARG;
+    p.q_in = q;
+    p.s_in = scales;
+    p.h = u;
+    p.ldh = p.ldu;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int halves = d->act == MOE_ACT_SWIGLU ? 2 : 1;
+    auto *k = d->dtype == MOE_F32
+                  ? (d->format == MOE_CKPT_INT8 ? ckpt::load_kernel<float, ckpt::INT8>
+                                                : ckpt::load_kernel<float, ckpt::E4M3>)
+                  : (d->format == MOE_CKPT_INT8 ? ckpt::load_kernel<__nv_bfloat16, ckpt::INT8>
+                                                : ckpt::load_kernel<__nv_bfloat16, ckpt::E4M3>);
+    return launch_pdl(k, ckpt_grid(p), dim3(ckpt::kThreads), 0, s, p, halves);
+}
+
+int moe_ckpt_backward(const moe_ckpt *d, const uint8_t *q, const uint8_t *scales, int64_t rows, const void *dh,
+                      const float *w, void *du, void *hw, float *dw, moe_stream_t stream) {
+    ckpt::Params p;
+    MOE_TRY(make_ckpt_params(d, rows, &p));
+    if (d->act == MOE_ACT_NONE) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!q || !scales || !dh || !du) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(dh) || !aligned16(du) || !aligned16(hw) || !aligned4(w) || !aligned4(dw))
+        return MOE_ERR_INVALID_ARG;
+    p.q_in = q;
+    p.s_in = scales;
+    p.dh = dh;
+    p.w = w;
+    p.du = du;
+    p.hw = hw;
+    p.dw = dw;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (d->dtype == MOE_F32)
+        return d->format == MOE_CKPT_INT8 ? launch_ckpt_backward<float, ckpt::INT8>(d->act, p, s)
+                                          : launch_ckpt_backward<float, ckpt::E4M3>(d->act, p, s);
+    return d->format == MOE_CKPT_INT8 ? launch_ckpt_backward<__nv_bfloat16, ckpt::INT8>(d->act, p, s)
+                                      : launch_ckpt_backward<__nv_bfloat16, ckpt::E4M3>(d->act, p, s);
+}
+
+int moe_q4_quantize(const moe_q4 *d, const void *W, int32_t w_dtype, uint8_t *codes, void *scales,
+                    moe_stream_t stream) {
+    q4::Params p;
+    MOE_TRY(make_q4_params(d, &p));
+    if (!dtype_ok(w_dtype)) return MOE_ERR_INVALID_ARG;
+    if (!W || !codes || !scales || !aligned16(W) || !aligned16(codes) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
+    DeviceInfo *dev = nullptr;
+    MOE_TRY(device_info(&dev));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t rows = (int64_t)p.N * p.n;
+    const dim3 grid((unsigned)std::min<int64_t>(cdiv(rows * p.groups, q4::kThreads / 32), (int64_t)dev->sms * 32));
+    if (w_dtype == MOE_F32) {
+        auto *k = d->format == MOE_Q4_INT4 ? q4::quantize_kernel<q4::INT4, float> : q4::quantize_kernel<q4::E2M1, float>;
+        return launch_pdl(k, grid, dim3(q4::kThreads), 0, s, static_cast<const float *>(W), rows, p.k, p.group_shift,
+                          p.groups, codes, scales);
+    }
+    auto *k = d->format == MOE_Q4_INT4 ? q4::quantize_kernel<q4::INT4, __nv_bfloat16>
+                                       : q4::quantize_kernel<q4::E2M1, __nv_bfloat16>;
+    return launch_pdl(k, grid, dim3(q4::kThreads), 0, s, static_cast<const __nv_bfloat16 *>(W), rows, p.k,
+                      p.group_shift, p.groups, codes, scales);
+}
+
+int moe_q4_dequantize(const moe_q4 *d, const uint8_t *codes, const void *scales, void *W, int32_t w_dtype,
+                      moe_stream_t stream) {
+    q4::Params p;
+    MOE_TRY(make_q4_params(d, &p));
+    if (!dtype_ok(w_dtype)) return MOE_ERR_INVALID_ARG;
+    if (!W || !codes || !scales || !aligned16(W) || !aligned16(codes) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
+    DeviceInfo *dev = nullptr;
+    MOE_TRY(device_info(&dev));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t rows = (int64_t)p.N * p.n;
+    const dim3 grid((unsigned)std::min<int64_t>(cdiv(rows * (p.k / 8), q4::kThreads), (int64_t)dev->sms * 32));
+    if (w_dtype == MOE_F32) {
+        auto *k = d->format == MOE_Q4_INT4 ? q4::dequantize_kernel<q4::INT4, float>
+                                           : q4::dequantize_kernel<q4::E2M1, float>;
+        return launch_pdl(k, grid, dim3(q4::kThreads), 0, s, codes, scales, rows, p.k, p.group_shift, p.groups,
+                          static_cast<float *>(W));
+    }
+    auto *k = d->format == MOE_Q4_INT4 ? q4::dequantize_kernel<q4::INT4, __nv_bfloat16>
+                                       : q4::dequantize_kernel<q4::E2M1, __nv_bfloat16>;
+    return launch_pdl(k, grid, dim3(q4::kThreads), 0, s, codes, scales, rows, p.k, p.group_shift, p.groups,
+                      static_cast<__nv_bfloat16 *>(W));
+}
+
+int moe_q4_matvec(const moe_q4 *d, const void *x, int64_t pairs, int32_t x_div, const int32_t *expert,
+                  const uint8_t *codes, const void *scales, const float *gate, void *y, int32_t y_dtype,
+                  moe_stream_t stream) {
+    q4::Params p;
+    MOE_TRY(make_q4_params(d, &p));
+    if (pairs < 0 || x_div < 1 || !dtype_ok(y_dtype)) return MOE_ERR_INVALID_ARG;
+    if (pairs > kQ4MaxPairs) return MOE_ERR_UNSUPPORTED;
+    if (pairs == 0) return MOE_OK;
+    if (!x || !expert || !codes || !scales || !y) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) || !aligned16(y) || !aligned4(expert) || !aligned4(gate))
+        return MOE_ERR_INVALID_ARG;
+    p.x = static_cast<const __nv_bfloat16 *>(x);
+    p.pairs = pairs;
+    p.x_div = x_div;
+    p.expert = expert;
+    p.codes = codes;
+    p.scales = scales;
+    p.gate = gate;
+    p.y = y;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (d->format == MOE_Q4_INT4) return launch_q4_act<q4::INT4>(d->act, p, y_dtype, s);
+    return launch_q4_act<q4::E2M1>(d->act, p, y_dtype, s);
+}
+
+}  // extern "C"
