@@ -20,6 +20,7 @@
 #include "moe_gemm_decode.cuh"
 #include "moe_gemm_tc.cuh"
 #include "moe_grouped_mm.cuh"
+#include "moe_grouped_mm_tc.cuh"
 #include "moe_q4.cuh"
 #include "moe_route.cuh"
 #include "moe_router_tc.cuh"
@@ -225,6 +226,8 @@ int allow_smem(K *kernel) {
                : MOE_ERR_CUDA;
 }
 
+int expert_ops_attrs();   // moe_expert_ops.cuh
+
 int device_info(DeviceInfo **out) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MOE_ERR_CUDA;
@@ -289,6 +292,7 @@ int device_info(DeviceInfo **out) {
         MOE_DEC_ATTR(32);
         MOE_DEC_ATTR(64);
 #undef MOE_DEC_ATTR
+        MOE_TRY(expert_ops_attrs());
         // Clusters need both CTAs in one GPC, so fewer than sms / 2 pairs may fit
         // at once; the persistent pair GEMM is launched with no more than fit
         // (at the largest shared-memory size it uses).

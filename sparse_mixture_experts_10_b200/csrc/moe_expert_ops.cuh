@@ -37,13 +37,15 @@ int make_gmm_plan(const moe_gmm *d, int64_t rows, GmmPlan *out) {
     if (d->n % (16 / es) || d->k % (16 / es)) return MOE_ERR_INVALID_ARG;
     gmm::Params &p = out->p;
     p = gmm::Params{};
-    const bool tn = d->kind == MOE_GMM_TN;
     out->a_cols = d->kind == MOE_GMM_NT ? d->k : d->n;
     out->c_cols = d->kind == MOE_GMM_NT ? d->n : d->k;
     MOE_TRY(take_stride(d->lda, out->a_cols, es, &p.lda));
     MOE_TRY(take_stride(d->ldb, d->k, es, &p.ldb));
     MOE_TRY(take_stride(d->ldc, out->c_cols, os, &p.ldc));
-    if (!tn && (double)d->groups * d->n * (double)p.ldb > 4e18) return MOE_ERR_INVALID_ARG;
+    // a tensor map's strides stay below 2^40 bytes
+    if ((int64_t)d->n * p.ldb * es >= (int64_t(1) << 40) || p.lda * es >= (int64_t(1) << 40) ||
+        (int64_t)d->n * p.ldc * os >= (int64_t(1) << 40))
+        return MOE_ERR_UNSUPPORTED;
     p.rows = rows;
     p.G = d->groups;
     p.n = d->n;
@@ -70,11 +72,70 @@ int launch_gmm_simt(gmm::Params p, const DeviceInfo &dev, cudaStream_t s) {
     return launch_pdl(gmm::simt_kernel<T, TO, KIND>, dim3(grid), dim3(256), 0, s, p);
 }
 
+// bf16 [d2, d1, d0] with strides of s1 and s2 elements; boxes of b1 x 64, 128-byte swizzle.
+int make_map3(CUtensorMap *m, const void *base, int64_t d0, int64_t d1, int64_t d2, int64_t s1, int64_t s2, int b1) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return MOE_ERR_CUDA;
+    const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
+    const cuuint64_t strides[2] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)b1, 1u};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <int KIND, typename TO>
+int launch_gmm_tc(gmm::Params p, const DeviceInfo &dev, cudaStream_t s) {
+    CUtensorMap mm, mn;
+    if (KIND == gmm::TN) {
+        MOE_TRY(make_map3(&mm, p.B, p.k, p.rows, 1, p.ldb, p.ldb, 64));
+        MOE_TRY(make_map3(&mn, p.A, p.n, p.rows, 1, p.lda, p.lda, 64));
+    } else {
+        MOE_TRY(make_map3(&mm, p.B, p.k, p.n, p.G, p.ldb, (int64_t)p.n * p.ldb, KIND == gmm::NT ? 128 : 64));
+        MOE_TRY(make_map3(&mn, p.A, KIND == gmm::NT ? p.k : p.n, p.rows, 1, p.lda, p.lda, gmm::kRowBox));
+    }
+    const int64_t F = KIND == gmm::NT ? p.n : p.k, live = std::min<int64_t>(p.G, p.rows);
+    // row tiles of 256 there are at least; segments are on the device, so this is what the host knows
+    const int64_t row_tiles = KIND == gmm::TN ? (int64_t)p.G * cdiv(p.n, 256) : std::max(live, cdiv(p.rows, 256));
+    const bool pair = row_tiles * cdiv(F, 256) >= dev.pair_clusters;
+    const int unit = pair ? 256 : 128;
+    p.m_tiles = (int)cdiv(F, unit);
+    p.n_tiles = (int)cdiv(p.n, unit);
+    const int64_t upper = KIND == gmm::TN ? (int64_t)p.G * p.m_tiles * p.n_tiles
+                                          : (cdiv(p.rows, unit) + live) * p.m_tiles;
+    if (upper > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    p.total = (int)upper;
+    const size_t smem = gmm::tc_smem_bytes(p.G);
+    if (pair)
+        return launch_pdl(gmm::tc_pair_kernel<KIND, TO>,
+                          dim3((unsigned)(2 * std::min<int64_t>(upper, dev.pair_clusters))), dim3(gmm::kTcThreads),
+                          smem, s, mm, mn, p);
+    return launch_pdl(gmm::tc_single_kernel<KIND, TO>, dim3((unsigned)std::min<int64_t>(upper, dev.sms)),
+                      dim3(gmm::kTcThreads), smem, s, mm, mn, p);
+}
+
 template <int KIND>
 int launch_gmm(const moe_gmm *d, const gmm::Params &p, const DeviceInfo &dev, cudaStream_t s) {
     if (d->dtype == MOE_F32) return launch_gmm_simt<float, float, KIND>(p, dev, s);
-    if (d->out_dtype == MOE_F32) return launch_gmm_simt<__nv_bfloat16, float, KIND>(p, dev, s);
-    return launch_gmm_simt<__nv_bfloat16, __nv_bfloat16, KIND>(p, dev, s);
+    if (d->out_dtype == MOE_F32) return launch_gmm_tc<KIND, float>(p, dev, s);
+    return launch_gmm_tc<KIND, __nv_bfloat16>(p, dev, s);
+}
+
+// Attributes of this file's kernels, set once per device with the others'.
+int expert_ops_attrs() {
+#define MOE_GMM_ATTR(KIND, TO)                              \
+    MOE_TRY(allow_smem(gmm::tc_pair_kernel<KIND, TO>));     \
+    MOE_TRY(allow_smem(gmm::tc_single_kernel<KIND, TO>))
+    MOE_GMM_ATTR(gmm::NT, float);
+    MOE_GMM_ATTR(gmm::NN, float);
+    MOE_GMM_ATTR(gmm::TN, float);
+    MOE_GMM_ATTR(gmm::NT, __nv_bfloat16);
+    MOE_GMM_ATTR(gmm::NN, __nv_bfloat16);
+    MOE_GMM_ATTR(gmm::TN, __nv_bfloat16);
+#undef MOE_GMM_ATTR
+    return MOE_OK;
 }
 
 // ---------------------------------------------------------------- 8-bit checkpoints

@@ -1,0 +1,411 @@
+// moe_grouped_mm_tc.cuh -- grouped products of bf16 operands on the tcgen05 tensor cores.
+//
+// Every kind is computed as  OUT[row, f] = sum_c M[f, c] N[row, c]  with the
+// contiguous index f of the result on the accumulator's lanes (the M side of
+// the instruction, fixed at 128 per CTA) and its rows on the accumulator's
+// columns (the N side, any multiple of 16):
+//          f      row            c         M operand          N operand
+//   NT     n      token row      k         b[g] K-major       a K-major
+//   NN     k      token row      n         b[g] MN-major      a K-major
+//   TN     k      n              token row b MN-major         a MN-major
+// The ragged length of a segment then sits on the side whose tile can have any
+// size: a segment of L rows is cut into ceil(L / 256) nearly equal tiles of a
+// multiple of 16 rows, and no tensor time goes into padding (with the rows on
+// the 256-row side a segment of 520 rows would pay for 768).
+//
+// One persistent CTA (kPair false: tiles of 128 x <=128) or CTA pair (tiles of
+// 256 x <=256, each CTA of the pair loads its 128 f's and half of the rows)
+// per SM; 352 threads:
+//   warps 0-7  epilogue: tcgen05.ld 32 columns at a time; a lane holds one f,
+//              so a warp writes 32 consecutive values of a row (bf16: two
+//              rows of pairs after a lane exchange)
+//   warp 8     TMA producer: 64-wide slices along c into a ring
+//   warp 9     issues tcgen05.mma into one of two accumulators
+//   warp 10    TN: clears the rows behind a segment's end in its last slice.
+//              Those rows belong to another expert (or to nobody) and may hold
+//              anything, NaN included, so both operands are cleared
+// Slices past the end of n or k are zero-filled by TMA: the weights' tensor map
+// has the group as its own dimension.
+//
+// Every wait is bounded; on expiry the waiting role stops issuing work, the
+// status word records MOE_STATUS_TIMEOUT and the CTA drains and returns.
+#pragma once
+
+#include "moe_gemm_tc.cuh"
+#include "moe_grouped_mm.cuh"
+
+#include <type_traits>
+
+namespace moe {
+namespace gmm {
+
+constexpr int kSl = 64;                 // slice along the contraction
+constexpr int kStages = 6;
+constexpr int kOpBytes = 128 * kSl * 2; // one operand of a stage, per CTA
+constexpr int kTcThreads = 32 * 11;
+constexpr int kRowBox = 32;             // rows of a TMA box of the K-major N operand
+
+__host__ __device__ constexpr size_t tc_smem_bytes(int groups) {
+    return 1024 + (size_t)kStages * 2 * kOpBytes + (3 * kStages + 5) * 8 + 16 + 8 * (size_t)(groups + 1);
+}
+
+// cp.async.bulk.tensor of a 3-D box; kPair: completion on the leader CTA's barrier.
+template <bool kPair>
+__device__ __forceinline__ void tma_load_3d(const CUtensorMap *map, uint32_t bar, void *dst, int c0, int c1, int c2) {
+    if (kPair)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+            "%4, %5}], [%2];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+            "%5}], [%2];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+            : "memory");
+}
+
+// Descriptor of an MN-major bf16 operand with 128-byte swizzle, written by TMA
+// as boxes of 64 (c) rows x 64 values: along MN, chunks of 64 values are one
+// box (8192 bytes) apart; along c, groups of 8 rows are 1024 bytes apart.
+// Advancing by 16 c's adds 2048 bytes.
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(8192u >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+struct Tile {
+    int g, f0, r0, rows, nsz;   // first f and row of the result; valid rows; N of the instruction
+    int c0, nc;                 // contraction start and length
+};
+
+template <int KIND, bool kPair>
+__device__ __forceinline__ Tile tile_at(const Params &p, const int *s_off, const int *s_cum, int i) {
+    constexpr int kM = kPair ? 256 : 128, kN = kPair ? 256 : 128;
+    Tile t;
+    if (KIND == TN) {
+        const int per = p.m_tiles * p.n_tiles;
+        t.g = i / per;
+        const int r = i - t.g * per;
+        t.f0 = r / p.n_tiles * kM;
+        t.r0 = (r % p.n_tiles) * kN;
+        t.rows = min(kN, p.n - t.r0);
+        // an MN-major N operand is made of whole chunks of 64 per CTA
+        t.nsz = t.rows > kN / 2 ? kN : kN / 2;
+        t.c0 = s_off[t.g];
+        t.nc = s_off[t.g + 1] - t.c0;
+    } else {
+        // tile order: expert, then f tile, then row tile, so that the tiles in flight share weights
+        int lo = 0, hi = p.G - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if ((int64_t)s_cum[mid] * p.m_tiles <= i) lo = mid;
+            else hi = mid - 1;
+        }
+        t.g = lo;
+        const int tiles = s_cum[lo + 1] - s_cum[lo];
+        const int r = i - s_cum[lo] * p.m_tiles;
+        t.f0 = r / tiles * kM;
+        const int len = s_off[lo + 1] - s_off[lo];
+        t.nsz = ((len + tiles - 1) / tiles + 15) & ~15;
+        const int at = r % tiles * t.nsz;
+        t.r0 = s_off[lo] + at;
+        t.rows = min(t.nsz, len - at);   // not positive for a last tile that the rounding left empty
+        t.c0 = 0;
+        t.nc = KIND == NT ? p.k : p.n;
+    }
+    return t;
+}
+
+// 32 accumulator columns (rows r0.. of the result) of this lane's f.
+template <typename TO>
+__device__ __forceinline__ void store_cols(TO *out, int64_t ldc, int f, bool f_ok, const uint32_t (&r)[32], int rows,
+                                           int accumulate) {
+    if (sizeof(TO) == 4) {
+        float *dst = reinterpret_cast<float *>(out) + f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if (j < rows && f_ok) {
+                const float v = __uint_as_float(r[j]);
+                dst[j * ldc] = accumulate ? dst[j * ldc] + v : v;
+            }
+        }
+    } else {
+        const int odd = threadIdx.x & 1;
+        __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(out) + (f & ~1) + (odd ? ldc : 0);
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {   // even lanes write row j, odd lanes row j + 1
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? r[j] : r[j + 1], 1);
+            float lo = __uint_as_float(odd ? got : r[j]), hi = __uint_as_float(odd ? r[j + 1] : got);
+            if (j + odd < rows && f_ok) {
+                uint32_t *q = reinterpret_cast<uint32_t *>(dst + j * ldc);
+                if (accumulate) {
+                    const uint32_t o = *q;
+                    lo += __uint_as_float(o << 16);
+                    hi += __uint_as_float(o & 0xffff0000u);
+                }
+                *q = pack_bf16x2(lo, hi);
+            }
+        }
+    }
+}
+
+template <int KIND, typename TO, bool kPair>
+__device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const CUtensorMap &tmN, const Params &p) {
+    pdl_enter();
+    constexpr int kAccCols = kPair ? 256 : 128;
+    constexpr bool kMmn = KIND != NT, kNmn = KIND == TN;   // MN-major operands
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = align_smem_1024(smem_raw);
+    uint8_t *sM = smem, *sN = smem + kStages * kOpBytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(sN + kStages * kOpBytes);
+    uint64_t *empty = full + kStages;
+    uint64_t *raw = empty + kStages;   // TN: a last slice has landed and is to be cleared
+    uint64_t *tfull = raw + kStages;
+    uint64_t *tempty = tfull + 2;
+    uint64_t *drain = tempty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    int *s_off = reinterpret_cast<int *>(tmem_slot + 4);
+    int *s_cum = s_off + p.G + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = kPair ? tc::cluster_ctarank() : 0;
+    const int first = kPair ? (int)tc::cluster_id_x() : (int)blockIdx.x;
+    const int step = kPair ? (int)tc::nclusters_x() : (int)gridDim.x;
+
+    if (warp == 0) load_segments(p.row_offsets, p.G, p.rows, kAccCols, s_off, s_cum);
+    if (warp == 8 && lane == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], KIND == TN && kPair ? 2 : 1);
+            mbar_init(&empty[s], 1);
+            mbar_init(&raw[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&tfull[a], 1);
+            mbar_init(&tempty[a], (kPair ? 2 : 1) * 8);
+        }
+        mbar_init(drain, 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&tmM);
+        tma_prefetch_desc(&tmN);
+    }
+    if (warp == 9) {
+        if (kPair) tc::tmem_alloc2(tmem_slot, 2 * kAccCols);
+        else tmem_alloc(tmem_slot, 2 * kAccCols);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (kPair) tc::cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int total = KIND == TN ? p.total : s_cum[p.G] * p.m_tiles;
+
+    if (warp == 8) {
+        // ------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            IssuedSlots iss, iss_raw;
+            uint32_t raw_phase = 0;
+            for (int i = first; i < total && ok; i += step) {
+                const Tile t = tile_at<KIND, kPair>(p, s_off, s_cum, i);
+                if (KIND != TN && t.rows <= 0) continue;
+                const int f = t.f0 + (int)rank * 128;
+                const int half = kPair ? t.nsz / 2 : t.nsz;   // N rows this CTA loads
+                const int r = t.r0 + (int)rank * half;
+                const int boxes = kNmn ? (half + 63) / 64 : (half + kRowBox - 1) / kRowBox;
+                const uint32_t bytes = kOpBytes + boxes * (kNmn ? 64 * 128 : kRowBox * 128);
+                const int nkb = (t.nc + kSl - 1) / kSl;
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (!mbar_wait(&empty[stage], phase ^ 1, p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const int c = t.c0 + kb * kSl;
+                    uint8_t *dM = sM + stage * kOpBytes, *dN = sN + stage * kOpBytes;
+                    auto loads = [&](auto pair, uint32_t bar) {
+                        constexpr bool P = decltype(pair)::value;
+                        if (KIND == NT) {
+                            tma_load_3d<P>(&tmM, bar, dM, c, f, t.g);
+                        } else {
+                            const int z = KIND == NN ? t.g : 0;
+                            tma_load_3d<P>(&tmM, bar, dM, f, c, z);
+                            tma_load_3d<P>(&tmM, bar, dM + 8192, f + 64, c, z);
+                        }
+                        for (int b = 0; b < boxes; ++b) {
+                            if (kNmn) tma_load_3d<P>(&tmN, bar, dN + b * 8192, r + b * 64, c, 0);
+                            else tma_load_3d<P>(&tmN, bar, dN + b * kRowBox * 128, c, r + b * kRowBox, 0);
+                        }
+                    };
+                    if (KIND == TN && kb == nkb - 1 && t.nc % kSl != 0) {   // warp 10 passes it on
+                        mbar_arrive_expect_tx(&raw[stage], bytes);
+                        loads(std::false_type{}, smem_u32(&raw[stage]));
+                        iss_raw.note(stage, (raw_phase >> stage) & 1u);
+                        raw_phase ^= 1u << stage;
+                    } else {
+                        if (rank == 0) mbar_arrive_expect_tx(&full[stage], (kPair ? 2 : 1) * bytes);
+                        else if (KIND == TN) tc::mbar_arrive_remote(tc::mapa_shared(smem_u32(&full[stage]), 0));
+                        loads(std::integral_constant<bool, kPair>{},
+                              kPair ? tc::mapa_shared(smem_u32(&full[stage]), 0) : smem_u32(&full[stage]));
+                        iss.note(stage, phase);
+                    }
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (!ok) {   // copies in flight land before the CTA leaves (a pair's land on the leader's barriers)
+                iss_raw.drain(raw, p.timeout_ns);
+                if (rank == 0) iss.drain(full, p.timeout_ns);
+            }
+        }
+    } else if (warp == 9) {
+        // ------------------------------------------------------------ MMA issuer (leader CTA)
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t kIdesc = idesc_bf16_f32(kPair ? 256 : 128, 0) | (kMmn ? 1u << 15 : 0u) |
+                                        (kNmn ? 1u << 16 : 0u);
+            int stage = 0;
+            uint32_t phase = 0;
+            int local = 0;
+            bool ok = true;
+            for (int i = first; i < total && ok; i += step) {
+                const Tile t = tile_at<KIND, kPair>(p, s_off, s_cum, i);
+                if (KIND == TN ? t.nc == 0 : t.rows <= 0) continue;
+                const int a = local & 1;
+                const uint32_t aph = (local >> 1) & 1;
+                ++local;
+                if (!(kPair ? tc::mbar_wait_cluster(&tempty[a], aph ^ 1, p.timeout_ns)
+                            : mbar_wait(&tempty[a], aph ^ 1, p.timeout_ns))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + a * kAccCols;
+                const uint32_t idesc = kIdesc | (static_cast<uint32_t>(t.nsz >> 3) << 17);
+                const int nkb = (t.nc + kSl - 1) / kSl;
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (!(KIND == TN && kPair ? tc::mbar_wait_cluster(&full[stage], phase, p.timeout_ns)
+                                              : mbar_wait(&full[stage], phase, p.timeout_ns))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t aM = smem_u32(sM + stage * kOpBytes), aN = smem_u32(sN + stage * kOpBytes);
+                    const uint64_t dm = kMmn ? smem_desc_mn(aM) : smem_desc_sw128(aM);
+                    const uint64_t dn = kNmn ? smem_desc_mn(aN) : smem_desc_sw128(aN);
+#pragma unroll
+                    for (int k = 0; k < kSl / 16; ++k) {
+                        const uint64_t m = dm + (kMmn ? 128 : 2) * k, n = dn + (kNmn ? 128 : 2) * k;
+                        if (kPair) tc::tc_mma2_bf16(d_tmem, m, n, idesc, (kb | k) != 0 ? 1u : 0u);
+                        else tc_mma_bf16(d_tmem, m, n, idesc, (kb | k) != 0 ? 1u : 0u);
+                    }
+                    if (kPair) tc::tc_commit2_mc(&empty[stage], 0x3);
+                    else tc_commit(&empty[stage]);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (ok) {
+                    if (kPair) tc::tc_commit2_mc(&tfull[a], 0x3);
+                    else tc_commit(&tfull[a]);
+                }
+            }
+            if (!ok) {   // wait (bounded) for the MMAs already issued before TMEM is freed
+                if (kPair) tc::tc_commit2(drain);
+                else tc_commit(drain);
+                mbar_wait(drain, 0, p.timeout_ns);
+            }
+        }
+    } else if (warp == 10) {
+        // ------------------------------------------------------------ TN: rows behind the segment's end
+        if (KIND == TN) {
+            int it = 0;
+            uint32_t raw_phase = 0;
+            for (int i = first; i < total; i += step) {
+                const Tile t = tile_at<KIND, kPair>(p, s_off, s_cum, i);
+                const int nkb = (t.nc + kSl - 1) / kSl, left = t.nc % kSl;
+                it += nkb;
+                if (left == 0) continue;
+                const int stage = (it - 1) % kStages;
+                if (!__all_sync(0xffffffffu, mbar_wait(&raw[stage], (raw_phase >> stage) & 1u, p.timeout_ns))) break;
+                raw_phase ^= 1u << stage;
+                const int n16 = (kSl - left) * 8;   // 16-byte pieces of the cleared rows in each box
+                for (int b = 0; b < 4; ++b) {
+                    uint4 *q = reinterpret_cast<uint4 *>((b < 2 ? sM : sN) + stage * kOpBytes + (b & 1) * 8192) + left * 8;
+                    for (int j = lane; j < n16; j += 32) q[j] = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (kPair) tc::mbar_arrive_remote(tc::mapa_shared(smem_u32(&full[stage]), 0));
+                    else mbar_arrive(&full[stage]);
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        const int q = warp & 3, part = warp >> 2;
+        int local = 0;
+        for (int i = first; i < total; i += step) {
+            const Tile t = tile_at<KIND, kPair>(p, s_off, s_cum, i);
+            if (t.rows <= 0) continue;
+            const int f = t.f0 + (int)rank * 128 + q * 32 + lane;
+            const bool f_ok = f < (KIND == NT ? p.n : p.k);
+            TO *out = static_cast<TO *>(p.C) + ((KIND == TN ? (int64_t)t.g * p.n : 0) + t.r0) * p.ldc;
+            if (KIND == TN && t.nc == 0) {   // an expert without rows: its gradient is zero
+                if (!p.accumulate && f_ok)
+                    for (int j = part; j < t.rows; j += 2) out[j * p.ldc + f] = TO(0.0f);
+                continue;
+            }
+            const int a = local & 1;
+            const uint32_t aph = (local >> 1) & 1;
+            ++local;
+            // warp-uniform decision: the TMEM loads below are warp-collective
+            if (!__all_sync(0xffffffffu, mbar_wait(&tfull[a], aph, p.timeout_ns))) break;
+            tc_fence_after();
+            const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * kAccCols;
+            for (int c = part * 32; c < t.rows; c += 64) {
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(tb + c, r);
+                tmem_ld_wait();
+                store_cols(out + c * p.ldc, p.ldc, f, f_ok, r, t.rows - c, KIND == TN ? p.accumulate : 0);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (kPair) tc::mbar_arrive_remote(tc::mapa_shared(smem_u32(&tempty[a]), 0));
+                else mbar_arrive(&tempty[a]);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (kPair) tc::cluster_sync();   // the leader's last MMAs read this CTA's shared memory and TMEM
+    if (warp == 9) {
+        tc_fence_after();
+        if (kPair) tc::tmem_dealloc2(tmem_base, 2 * kAccCols);
+        else tmem_dealloc(tmem_base, 2 * kAccCols);
+    }
+}
+
+template <int KIND, typename TO>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
+    tc_pair_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_constant__ CUtensorMap tmN, const Params p) {
+    tc_body<KIND, TO, true>(tmM, tmN, p);
+}
+template <int KIND, typename TO>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    tc_single_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_constant__ CUtensorMap tmN, const Params p) {
+    tc_body<KIND, TO, false>(tmM, tmN, p);
+}
+
+}  // namespace gmm
+}  // namespace moe

@@ -121,7 +121,8 @@ TYPES = [(BF, BF), (BF, F32), (F32, F32)]
 @pytest.mark.parametrize("dt,out", TYPES)
 @pytest.mark.parametrize("lengths,n,k", [
     ([1], 8, 8), ([0, 1, 0], 64, 64), ([5, 0, 130, 64, 1], 72, 200), ([129, 127, 256, 1, 0, 63], 264, 136),
-    ([300, 17], 520, 72), ([2, 3, 65], 8, 1032), ([513], 256, 256), ([0, 0, 0], 32, 16), ([700, 0, 33, 257], 384, 512)])
+    ([300, 17], 520, 72), ([2, 3, 65], 8, 1032), ([513], 256, 256), ([0, 0, 0], 32, 16), ([700, 0, 33, 257], 384, 512),
+    ([300, 0, 1, 777, 129], 4104, 1000), ([130, 600, 2, 0, 511], 1000, 4104)])
 def test_grouped_mm(kind, dt, out, lengths, n, k):
     if sum(lengths) == 0 and kind != moe.MOE_GMM_TN:
         gmm_case(kind, lengths, n, k, dt, out, extra=5)
