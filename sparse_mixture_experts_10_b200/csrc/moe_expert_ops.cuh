@@ -72,34 +72,58 @@ int launch_gmm_simt(gmm::Params p, const DeviceInfo &dev, cudaStream_t s) {
     return launch_pdl(gmm::simt_kernel<T, TO, KIND>, dim3(grid), dim3(256), 0, s, p);
 }
 
-// bf16 [d2, d1, d0] with strides of s1 and s2 elements; boxes of b1 x 64, 128-byte swizzle.
-int make_map3(CUtensorMap *m, const void *base, int64_t d0, int64_t d1, int64_t d2, int64_t s1, int64_t s2, int b1) {
+// bf16 tensor of up to four dimensions (d[0] contiguous, the others with strides of st elements), 128-byte swizzle.
+int make_map_nd(CUtensorMap *m, int nd, const void *base, const int64_t *d, const int64_t *st, const int *box) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return MOE_ERR_CUDA;
-    const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
-    const cuuint64_t strides[2] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2};
-    const cuuint32_t box[3] = {64u, (cuuint32_t)b1, 1u};
-    const cuuint32_t estr[3] = {1u, 1u, 1u};
-    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    cuuint64_t dims[4], strides[3];
+    cuuint32_t b[4], estr[4];
+    for (int i = 0; i < nd; ++i) {
+        dims[i] = (cuuint64_t)d[i];
+        if (i) strides[i - 1] = (cuuint64_t)st[i - 1] * 2;
+        b[i] = (cuuint32_t)box[i];
+        estr[i] = 1;
+    }
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)nd, const_cast<void *>(base), dims, strides,
+                           b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
+}
+// K-major operand [G, rows, cols]: boxes of `box` rows x 64 columns.
+int make_map_k(CUtensorMap *m, const void *base, int64_t G, int64_t rows, int64_t cols, int64_t ld, int box) {
+    const int64_t d[3] = {cols, rows, G}, st[2] = {ld, G > 1 ? rows * ld : ld};
+    const int b[3] = {64, box, 1};
+    return make_map_nd(m, 3, base, d, st, b);
+}
+// MN-major operand [G, rows, cols]: boxes of 64 rows x two chunks of 64 columns where the width has whole
+// chunks only (*chunks), else of 64 rows x 64 columns.
+int make_map_mn(CUtensorMap *m, const void *base, int64_t G, int64_t rows, int64_t cols, int64_t ld, int *chunks) {
+    *chunks = cols % 64 == 0;
+    const int64_t gs = G > 1 ? rows * ld : ld;
+    const int64_t d[4] = {*chunks ? 64 : cols, rows, *chunks ? cols / 64 : 1, G}, st[3] = {ld, 64, gs};
+    const int b[4] = {64, 64, *chunks ? 2 : 1, 1};
+    return make_map_nd(m, 4, base, d, st, b);
 }
 
 template <int KIND, typename TO>
 int launch_gmm_tc(gmm::Params p, const DeviceInfo &dev, cudaStream_t s) {
-    CUtensorMap mm, mn;
+    CUtensorMap mm;
+    gmm::NMaps mn;
+    if (KIND == gmm::NT) MOE_TRY(make_map_k(&mm, p.B, p.G, p.n, p.k, p.ldb, 128));
+    else MOE_TRY(make_map_mn(&mm, p.B, KIND == gmm::NN ? p.G : 1, KIND == gmm::NN ? p.n : p.rows, p.k, p.ldb,
+                             &p.m_chunks));
     if (KIND == gmm::TN) {
-        MOE_TRY(make_map3(&mm, p.B, p.k, p.rows, 1, p.ldb, p.ldb, 64));
-        MOE_TRY(make_map3(&mn, p.A, p.n, p.rows, 1, p.lda, p.lda, 64));
+        MOE_TRY(make_map_mn(&mn.m[0], p.A, 1, p.rows, p.n, p.lda, &p.n_chunks));
+        for (int i = 1; i < 8; ++i) mn.m[i] = mn.m[0];
     } else {
-        MOE_TRY(make_map3(&mm, p.B, p.k, p.n, p.G, p.ldb, (int64_t)p.n * p.ldb, KIND == gmm::NT ? 128 : 64));
-        MOE_TRY(make_map3(&mn, p.A, KIND == gmm::NT ? p.k : p.n, p.rows, 1, p.lda, p.lda, gmm::kRowBox));
+        for (int i = 0; i < 8; ++i)
+            MOE_TRY(make_map_k(&mn.m[i], p.A, 1, p.rows, KIND == gmm::NT ? p.k : p.n, p.lda, 16 * (i + 1)));
     }
     const int64_t F = KIND == gmm::NT ? p.n : p.k, live = std::min<int64_t>(p.G, p.rows);
-    // row tiles of 256 there are at least; segments are on the device, so this is what the host knows
-    const int64_t row_tiles = KIND == gmm::TN ? (int64_t)p.G * cdiv(p.n, 256) : std::max(live, cdiv(p.rows, 256));
-    const bool pair = row_tiles * cdiv(F, 256) >= dev.pair_clusters;
+    // row tiles there are at least (segments are on the device; this is what the host knows)
+    auto row_tiles = [&](int64_t unit) { return std::max(live, cdiv(p.rows, unit)); };
+    const bool pair = (KIND == gmm::TN ? p.G * cdiv(p.n, 256) : row_tiles(256)) * cdiv(F, 256) >= dev.pair_clusters;
+    const bool wide = pair && KIND != gmm::TN && p.rows > 256 * live && row_tiles(512) * cdiv(F, 256) >= dev.pair_clusters;
     const int unit = pair ? 256 : 128;
     p.m_tiles = (int)cdiv(F, unit);
     p.n_tiles = (int)cdiv(p.n, unit);
@@ -108,10 +132,13 @@ int launch_gmm_tc(gmm::Params p, const DeviceInfo &dev, cudaStream_t s) {
     if (upper > INT32_MAX) return MOE_ERR_UNSUPPORTED;
     p.total = (int)upper;
     const size_t smem = gmm::tc_smem_bytes(p.G);
-    if (pair)
-        return launch_pdl(gmm::tc_pair_kernel<KIND, TO>,
-                          dim3((unsigned)(2 * std::min<int64_t>(upper, dev.pair_clusters))), dim3(gmm::kTcThreads),
-                          smem, s, mm, mn, p);
+    if (pair) {
+        const dim3 grid((unsigned)(2 * std::min<int64_t>(upper, dev.pair_clusters)));
+        if constexpr (KIND != gmm::TN)
+            if (wide)
+                return launch_pdl(gmm::tc_pair_kernel<KIND, TO, true>, grid, dim3(gmm::kTcThreads), smem, s, mm, mn, p);
+        return launch_pdl(gmm::tc_pair_kernel<KIND, TO, false>, grid, dim3(gmm::kTcThreads), smem, s, mm, mn, p);
+    }
     return launch_pdl(gmm::tc_single_kernel<KIND, TO>, dim3((unsigned)std::min<int64_t>(upper, dev.sms)),
                       dim3(gmm::kTcThreads), smem, s, mm, mn, p);
 }
@@ -125,15 +152,18 @@ int launch_gmm(const moe_gmm *d, const gmm::Params &p, const DeviceInfo &dev, cu
 
 // Attributes of this file's kernels, set once per device with the others'.
 int expert_ops_attrs() {
-#define MOE_GMM_ATTR(KIND, TO)                              \
-    MOE_TRY(allow_smem(gmm::tc_pair_kernel<KIND, TO>));     \
-    MOE_TRY(allow_smem(gmm::tc_single_kernel<KIND, TO>))
-    MOE_GMM_ATTR(gmm::NT, float);
-    MOE_GMM_ATTR(gmm::NN, float);
-    MOE_GMM_ATTR(gmm::TN, float);
-    MOE_GMM_ATTR(gmm::NT, __nv_bfloat16);
-    MOE_GMM_ATTR(gmm::NN, __nv_bfloat16);
-    MOE_GMM_ATTR(gmm::TN, __nv_bfloat16);
+#define MOE_GMM_ATTR(KIND)                                                     \
+    MOE_TRY(allow_smem(gmm::tc_pair_kernel<KIND, float, false>));              \
+    MOE_TRY(allow_smem(gmm::tc_single_kernel<KIND, float>));                   \
+    MOE_TRY(allow_smem(gmm::tc_pair_kernel<KIND, __nv_bfloat16, false>));      \
+    MOE_TRY(allow_smem(gmm::tc_single_kernel<KIND, __nv_bfloat16>))
+    MOE_GMM_ATTR(gmm::NT);
+    MOE_GMM_ATTR(gmm::NN);
+    MOE_GMM_ATTR(gmm::TN);
+    MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NT, float, true>));
+    MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NT, __nv_bfloat16, true>));
+    MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NN, float, true>));
+    MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NN, __nv_bfloat16, true>));
 #undef MOE_GMM_ATTR
     return MOE_OK;
 }

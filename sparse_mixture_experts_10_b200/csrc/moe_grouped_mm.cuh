@@ -78,7 +78,8 @@ struct Params {
     int G, n, k;
     int accumulate;           // TN: add to C
     int m_tiles, n_tiles;     // TN: tiles of a group; NT, NN: n_tiles column tiles
-    int total;                // TN: all tiles; NT, NN: -1 (known on the device)
+    int total;                // TN: all tiles; NT, NN: at most so many (the count is known on the device)
+    int m_chunks, n_chunks;   // tensor cores: an MN-major operand's map has chunks of 64 values as a dimension
     uint64_t timeout_ns;
 };
 

@@ -40,14 +40,22 @@ namespace moe {
 namespace gmm {
 
 constexpr int kSl = 64;                 // slice along the contraction
-constexpr int kStages = 6;
-constexpr int kOpBytes = 128 * kSl * 2; // one operand of a stage, per CTA
+constexpr int kOpBytes = 128 * kSl * 2; // 128 values of either side of a slice
 constexpr int kTcThreads = 32 * 11;
-constexpr int kRowBox = 32;             // rows of a TMA box of the K-major N operand
+constexpr int kMaxStages = 6;
 
+// Slices in the ring: 192 KB of shared memory either way.
+__host__ __device__ constexpr int ring_stages(bool wide) { return wide ? 4 : 6; }
 __host__ __device__ constexpr size_t tc_smem_bytes(int groups) {
-    return 1024 + (size_t)kStages * 2 * kOpBytes + (3 * kStages + 5) * 8 + 16 + 8 * (size_t)(groups + 1);
+    return 1024 + (size_t)12 * kOpBytes + (4 * kMaxStages + 5) * 8 + 16 + 8 * (size_t)(groups + 1);
 }
+
+// The N operand's tensor maps: K-major boxes of 16, 32, ... 128 rows, so that a slice is one copy of
+// just the tile's rows (192-row tiles in copies of 32 rows ran at 930 TFLOP/s, in one of 96 at 1166); TN uses
+// the first.
+struct NMaps {
+    CUtensorMap m[8];
+};
 
 // cp.async.bulk.tensor of a 3-D box; kPair: completion on the leader CTA's barrier.
 template <bool kPair>
@@ -66,6 +74,36 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap *map, uint32_t bar
             : "memory");
 }
 
+// The same for a 4-D box (64-value chunks of an MN-major operand).
+template <bool kPair>
+__device__ __forceinline__ void tma_load_4d(const CUtensorMap *map, uint32_t bar, void *dst, int c0, int c1, int c2,
+                                            int c3) {
+    if (kPair)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+            "%4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+            "%5, %6}], [%2];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+            : "memory");
+}
+// 128 values x 64 c's of an MN-major operand: one copy of two 64-value chunks where the width is a
+// multiple of 64 (the map then has the chunk as a dimension), else a copy for each.
+template <bool kPair>
+__device__ __forceinline__ void load_mn(const CUtensorMap *map, bool chunks, uint32_t bar, uint8_t *dst, int v, int c,
+                                        int g) {
+    if (chunks) {
+        tma_load_4d<kPair>(map, bar, dst, 0, c, v >> 6, g);
+    } else {
+        tma_load_4d<kPair>(map, bar, dst, v, c, 0, g);
+        tma_load_4d<kPair>(map, bar, dst + kOpBytes / 2, v + 64, c, 0, g);
+    }
+}
+
 // Descriptor of an MN-major bf16 operand with 128-byte swizzle, written by TMA
 // as boxes of 64 (c) rows x 64 values: along MN, chunks of 64 values are one
 // box (8192 bytes) apart; along c, groups of 8 rows are 1024 bytes apart.
@@ -80,15 +118,32 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
     return d;
 }
 
+// Hands an accumulator back to the leader's MMA thread.  Nothing but the (completed) TMEM loads before the
+// fence::before_thread_sync is ordered by it, so it is relaxed: a release at cluster scope would first wait for
+// this warp's stores of the result.
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t bar_cluster) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
+// One lane of the (converged) warp.  The issuing warps run their loops with all lanes and only the copies and
+// tensor instructions under this predicate: their descriptors then stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 struct Tile {
-    int g, f0, r0, rows, nsz;   // first f and row of the result; valid rows; N of the instruction
+    int g, f0, r0, rows;        // first f and row of the result; valid rows
+    int nh, nsub;               // N of one instruction, instructions side by side (kWide: up to two)
     int c0, nc;                 // contraction start and length
 };
 
-template <int KIND, bool kPair>
+template <int KIND, bool kPair, bool kWide>
 __device__ __forceinline__ Tile tile_at(const Params &p, const int *s_off, const int *s_cum, int i) {
     constexpr int kM = kPair ? 256 : 128, kN = kPair ? 256 : 128;
     Tile t;
+    t.nsub = 1;
     if (KIND == TN) {
         const int per = p.m_tiles * p.n_tiles;
         t.g = i / per;
@@ -97,7 +152,7 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const int *s_off, const
         t.r0 = (r % p.n_tiles) * kN;
         t.rows = min(kN, p.n - t.r0);
         // an MN-major N operand is made of whole chunks of 64 per CTA
-        t.nsz = t.rows > kN / 2 ? kN : kN / 2;
+        t.nh = t.rows > kN / 2 ? kN : kN / 2;
         t.c0 = s_off[t.g];
         t.nc = s_off[t.g + 1] - t.c0;
     } else {
@@ -112,11 +167,12 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const int *s_off, const
         const int tiles = s_cum[lo + 1] - s_cum[lo];
         const int r = i - s_cum[lo] * p.m_tiles;
         t.f0 = r / tiles * kM;
-        const int len = s_off[lo + 1] - s_off[lo];
-        t.nsz = ((len + tiles - 1) / tiles + 15) & ~15;
-        const int at = r % tiles * t.nsz;
+        const int len = s_off[lo + 1] - s_off[lo], size = (len + tiles - 1) / tiles;
+        if (kWide && size > kN) t.nsub = 2;
+        t.nh = ((size + t.nsub - 1) / t.nsub + 15) & ~15;
+        const int at = r % tiles * t.nh * t.nsub;
         t.r0 = s_off[lo] + at;
-        t.rows = min(t.nsz, len - at);   // not positive for a last tile that the rounding left empty
+        t.rows = min(t.nh * t.nsub, len - at);   // not positive for a last tile that the rounding left empty
         t.c0 = 0;
         t.nc = KIND == NT ? p.k : p.n;
     }
@@ -156,19 +212,22 @@ __device__ __forceinline__ void store_cols(TO *out, int64_t ldc, int f, bool f_o
     }
 }
 
-template <int KIND, typename TO, bool kPair>
-__device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const CUtensorMap &tmN, const Params &p) {
+template <int KIND, typename TO, bool kPair, bool kWide>
+__device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN, const Params &p) {
     pdl_enter();
+    static_assert(!kWide || (kPair && KIND != TN), "wide tiles: CTA pairs, K-major N operand");
     constexpr int kAccCols = kPair ? 256 : 128;
+    constexpr int kStages = ring_stages(kWide), kNBytes = (kWide ? 2 : 1) * kOpBytes;
     constexpr bool kMmn = KIND != NT, kNmn = KIND == TN;   // MN-major operands
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = align_smem_1024(smem_raw);
     uint8_t *sM = smem, *sN = smem + kStages * kOpBytes;
-    uint64_t *full = reinterpret_cast<uint64_t *>(sN + kStages * kOpBytes);
+    uint64_t *full = reinterpret_cast<uint64_t *>(sN + kStages * kNBytes);
     uint64_t *empty = full + kStages;
     uint64_t *raw = empty + kStages;   // TN: a last slice has landed and is to be cleared
-    uint64_t *tfull = raw + kStages;
-    uint64_t *tempty = tfull + 2;
+    uint64_t *fixed = raw + kStages;   // TN: ... and has been, in every CTA of the pair
+    uint64_t *tfull = fixed + kStages; // an accumulator (kWide: [0], both) is complete
+    uint64_t *tempty = tfull + 2;      // an accumulator has been read
     uint64_t *drain = tempty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     int *s_off = reinterpret_cast<int *>(tmem_slot + 4);
@@ -178,12 +237,13 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const CUtensorMa
     const int first = kPair ? (int)tc::cluster_id_x() : (int)blockIdx.x;
     const int step = kPair ? (int)tc::nclusters_x() : (int)gridDim.x;
 
-    if (warp == 0) load_segments(p.row_offsets, p.G, p.rows, kAccCols, s_off, s_cum);
+    if (warp == 0) load_segments(p.row_offsets, p.G, p.rows, (kWide ? 2 : 1) * kAccCols, s_off, s_cum);
     if (warp == 8 && lane == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], KIND == TN && kPair ? 2 : 1);
+            mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
             mbar_init(&raw[s], 1);
+            mbar_init(&fixed[s], kPair ? 2 : 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&tfull[a], 1);
@@ -192,7 +252,8 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const CUtensorMa
         mbar_init(drain, 1);
         fence_mbar_init();
         tma_prefetch_desc(&tmM);
-        tma_prefetch_desc(&tmN);
+        tma_prefetch_desc(&tmN.m[0]);
+        if (!kNmn) tma_prefetch_desc(&tmN.m[7]);
     }
     if (warp == 9) {
         if (kPair) tc::tmem_alloc2(tmem_slot, 2 * kAccCols);
@@ -204,123 +265,136 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const CUtensorMa
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const int total = KIND == TN ? p.total : s_cum[p.G] * p.m_tiles;
+    auto tile = [&](int i) { return tile_at<KIND, kPair, kWide>(p, s_off, s_cum, i); };
 
     if (warp == 8) {
         // ------------------------------------------------------------ TMA producer
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            IssuedSlots iss, iss_raw;
-            uint32_t raw_phase = 0;
-            for (int i = first; i < total && ok; i += step) {
-                const Tile t = tile_at<KIND, kPair>(p, s_off, s_cum, i);
-                if (KIND != TN && t.rows <= 0) continue;
-                const int f = t.f0 + (int)rank * 128;
-                const int half = kPair ? t.nsz / 2 : t.nsz;   // N rows this CTA loads
-                const int r = t.r0 + (int)rank * half;
-                const int boxes = kNmn ? (half + 63) / 64 : (half + kRowBox - 1) / kRowBox;
-                const uint32_t bytes = kOpBytes + boxes * (kNmn ? 64 * 128 : kRowBox * 128);
-                const int nkb = (t.nc + kSl - 1) / kSl;
-                for (int kb = 0; kb < nkb; ++kb) {
-                    if (!mbar_wait(&empty[stage], phase ^ 1, p.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    const int c = t.c0 + kb * kSl;
-                    uint8_t *dM = sM + stage * kOpBytes, *dN = sN + stage * kOpBytes;
-                    auto loads = [&](auto pair, uint32_t bar) {
-                        constexpr bool P = decltype(pair)::value;
-                        if (KIND == NT) {
-                            tma_load_3d<P>(&tmM, bar, dM, c, f, t.g);
-                        } else {
-                            const int z = KIND == NN ? t.g : 0;
-                            tma_load_3d<P>(&tmM, bar, dM, f, c, z);
-                            tma_load_3d<P>(&tmM, bar, dM + 8192, f + 64, c, z);
-                        }
-                        for (int b = 0; b < boxes; ++b) {
-                            if (kNmn) tma_load_3d<P>(&tmN, bar, dN + b * 8192, r + b * 64, c, 0);
-                            else tma_load_3d<P>(&tmN, bar, dN + b * kRowBox * 128, c, r + b * kRowBox, 0);
-                        }
-                    };
-                    if (KIND == TN && kb == nkb - 1 && t.nc % kSl != 0) {   // warp 10 passes it on
-                        mbar_arrive_expect_tx(&raw[stage], bytes);
-                        loads(std::false_type{}, smem_u32(&raw[stage]));
-                        iss_raw.note(stage, (raw_phase >> stage) & 1u);
-                        raw_phase ^= 1u << stage;
-                    } else {
-                        if (rank == 0) mbar_arrive_expect_tx(&full[stage], (kPair ? 2 : 1) * bytes);
-                        else if (KIND == TN) tc::mbar_arrive_remote(tc::mapa_shared(smem_u32(&full[stage]), 0));
-                        loads(std::integral_constant<bool, kPair>{},
-                              kPair ? tc::mapa_shared(smem_u32(&full[stage]), 0) : smem_u32(&full[stage]));
-                        iss.note(stage, phase);
-                    }
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
-                }
-            }
-            if (!ok) {   // copies in flight land before the CTA leaves (a pair's land on the leader's barriers)
-                iss_raw.drain(raw, p.timeout_ns);
-                if (rank == 0) iss.drain(full, p.timeout_ns);
-            }
-        }
-    } else if (warp == 9) {
-        // ------------------------------------------------------------ MMA issuer (leader CTA)
-        if (lane == 0 && rank == 0) {
-            constexpr uint32_t kIdesc = idesc_bf16_f32(kPair ? 256 : 128, 0) | (kMmn ? 1u << 15 : 0u) |
-                                        (kNmn ? 1u << 16 : 0u);
-            int stage = 0;
-            uint32_t phase = 0;
-            int local = 0;
-            bool ok = true;
-            for (int i = first; i < total && ok; i += step) {
-                const Tile t = tile_at<KIND, kPair>(p, s_off, s_cum, i);
-                if (KIND == TN ? t.nc == 0 : t.rows <= 0) continue;
-                const int a = local & 1;
-                const uint32_t aph = (local >> 1) & 1;
-                ++local;
-                if (!(kPair ? tc::mbar_wait_cluster(&tempty[a], aph ^ 1, p.timeout_ns)
-                            : mbar_wait(&tempty[a], aph ^ 1, p.timeout_ns))) {
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        IssuedSlots iss, iss_raw;
+        uint32_t full_phase = 0, raw_phase = 0;   // one bit per stage: TN uses either barrier of a stage
+        for (int i = first; i < total && ok; i += step) {
+            const Tile t = tile(i);
+            if (KIND != TN && t.rows <= 0) continue;
+            const int f = t.f0 + (int)rank * 128;
+            const int half = kPair ? t.nh / 2 : t.nh;   // N rows of an instruction that this CTA loads
+            const int r = t.r0 + (int)rank * half;
+            const int box = kNmn ? 7 : (half + 15) / 16 - 1;   // K-major: (box + 1) * 16 rows
+            const uint32_t bytes = kOpBytes + t.nsub * (box + 1) * (kOpBytes / 8);
+            const CUtensorMap *mapN = &tmN.m[kNmn ? 0 : box];
+            const int nkb = (t.nc + kSl - 1) / kSl;
+            for (int kb = 0; kb < nkb; ++kb) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1, p.timeout_ns))) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + a * kAccCols;
-                const uint32_t idesc = kIdesc | (static_cast<uint32_t>(t.nsz >> 3) << 17);
-                const int nkb = (t.nc + kSl - 1) / kSl;
-                for (int kb = 0; kb < nkb; ++kb) {
-                    if (!(KIND == TN && kPair ? tc::mbar_wait_cluster(&full[stage], phase, p.timeout_ns)
-                                              : mbar_wait(&full[stage], phase, p.timeout_ns))) {
-                        ok = false;
-                        break;
+                const int c = t.c0 + kb * kSl;
+                uint8_t *dM = sM + stage * kOpBytes, *dN = sN + stage * kNBytes;
+                auto loads = [&](auto pair, uint32_t bar) {
+                    constexpr bool P = decltype(pair)::value;
+                    if (KIND == NT) tma_load_3d<P>(&tmM, bar, dM, c, f, t.g);
+                    else load_mn<P>(&tmM, p.m_chunks, bar, dM, f, c, KIND == NN ? t.g : 0);
+                    if (kNmn) {
+                        load_mn<P>(mapN, p.n_chunks, bar, dN, r, c, 0);
+                    } else {
+                        tma_load_3d<P>(mapN, bar, dN, c, r, 0);
+                        if (kWide && t.nsub == 2) tma_load_3d<P>(mapN, bar, dN + kOpBytes, c, r + t.nh, 0);
                     }
-                    tc_fence_after();
-                    const uint32_t aM = smem_u32(sM + stage * kOpBytes), aN = smem_u32(sN + stage * kOpBytes);
-                    const uint64_t dm = kMmn ? smem_desc_mn(aM) : smem_desc_sw128(aM);
-                    const uint64_t dn = kNmn ? smem_desc_mn(aN) : smem_desc_sw128(aN);
-#pragma unroll
-                    for (int k = 0; k < kSl / 16; ++k) {
-                        const uint64_t m = dm + (kMmn ? 128 : 2) * k, n = dn + (kNmn ? 128 : 2) * k;
-                        if (kPair) tc::tc_mma2_bf16(d_tmem, m, n, idesc, (kb | k) != 0 ? 1u : 0u);
-                        else tc_mma_bf16(d_tmem, m, n, idesc, (kb | k) != 0 ? 1u : 0u);
+                };
+                if (KIND == TN && kb == nkb - 1 && t.nc % kSl != 0) {   // warp 10 passes it on
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&raw[stage], bytes);
+                        loads(std::false_type{}, smem_u32(&raw[stage]));
                     }
-                    if (kPair) tc::tc_commit2_mc(&empty[stage], 0x3);
-                    else tc_commit(&empty[stage]);
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1;
+                    iss_raw.note(stage, (raw_phase >> stage) & 1u);
+                    raw_phase ^= 1u << stage;
+                } else {
+                    const uint32_t bar = smem_u32(&full[stage]);
+                    if (elect_one()) {
+                        if (rank == 0) mbar_arrive_expect_tx(&full[stage], (kPair ? 2 : 1) * bytes);
+                        loads(std::integral_constant<bool, kPair>{}, kPair ? tc::mapa_shared(bar, 0) : bar);
                     }
+                    iss.note(stage, (full_phase >> stage) & 1u);
+                    full_phase ^= 1u << stage;
                 }
-                if (ok) {
-                    if (kPair) tc::tc_commit2_mc(&tfull[a], 0x3);
-                    else tc_commit(&tfull[a]);
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1;
                 }
             }
+        }
+        if (!ok) {   // copies in flight land before the CTA leaves (a pair's land on the leader's barriers)
+            iss_raw.drain(raw, p.timeout_ns);
+            if (rank == 0) iss.drain(full, p.timeout_ns);
+        }
+    } else if (warp == 9) {
+        // ------------------------------------------------------------ MMA issuer (leader CTA)
+        if (rank == 0) {
+            constexpr uint32_t kIdesc = idesc_bf16_f32(kPair ? 256 : 128, 0) | (kMmn ? 1u << 15 : 0u) |
+                                        (kNmn ? 1u << 16 : 0u);
+            int stage = 0;
+            uint32_t full_phase = 0, fixed_phase = 0, acc_phase = 3;   // acc_phase: parity of each accumulator's last release
+            int local = 0;
+            bool ok = true;
+            for (int i = first; i < total && ok; i += step) {
+                const Tile t = tile(i);
+                if (KIND == TN ? t.nc == 0 : t.rows <= 0) continue;
+                const int a0 = kWide ? 0 : local & 1;
+                ++local;
+                const uint32_t idesc = kIdesc | (static_cast<uint32_t>(t.nh >> 3) << 17);
+                const int nkb = (t.nc + kSl - 1) / kSl;
+                const uint32_t d_tmem = tmem_base + a0 * kAccCols;
+                for (int a = a0; a < a0 + t.nsub && ok; ++a) {   // the accumulators have been read
+                    const uint32_t ph = (acc_phase >> a) & 1u;
+                    ok = __all_sync(0xffffffffu, kPair ? tc::mbar_wait_cluster(&tempty[a], ph, p.timeout_ns)
+                                                       : mbar_wait(&tempty[a], ph, p.timeout_ns));
+                    acc_phase ^= 1u << a;
+                }
+                for (int kb = 0; kb < nkb && ok; ++kb) {
+                    if (KIND == TN && kb == nkb - 1 && t.nc % kSl != 0) {   // written by threads too, maybe the other CTA's
+                        const uint32_t ph = (fixed_phase >> stage) & 1u;
+                        ok = __all_sync(0xffffffffu, kPair ? tc::mbar_wait_cluster(&fixed[stage], ph, p.timeout_ns)
+                                                           : mbar_wait(&fixed[stage], ph, p.timeout_ns));
+                        fixed_phase ^= 1u << stage;
+                    } else {
+                        ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], (full_phase >> stage) & 1u, p.timeout_ns));
+                        full_phase ^= 1u << stage;
+                    }
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t aM = smem_u32(sM + stage * kOpBytes), aN = smem_u32(sN + stage * kNBytes);
+                    const uint64_t dm = kMmn ? smem_desc_mn(aM) : smem_desc_sw128(aM);
+                    const uint64_t dn = kNmn ? smem_desc_mn(aN) : smem_desc_sw128(aN);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < kSl / 16; ++k) {
+                            const uint64_t m = dm + (kMmn ? 128 : 2) * k, n = dn + (kNmn ? 128 : 2) * k;
+                            const uint32_t acc = (kb | k) != 0 ? 1u : 0u;
+                            if (kPair) tc::tc_mma2_bf16(d_tmem, m, n, idesc, acc);
+                            else tc_mma_bf16(d_tmem, m, n, idesc, acc);
+                            // the two accumulators in turn, so that an instruction does not wait for the one before it
+                            if (kWide && t.nsub == 2)
+                                tc::tc_mma2_bf16(d_tmem + kAccCols, m, n + (kOpBytes >> 4), idesc, acc);
+                        }
+                        if (kPair) tc::tc_commit2_mc(&empty[stage], 0x3);
+                        else tc_commit(&empty[stage]);
+                    }
+                    __syncwarp();
+                    if (++stage == kStages) stage = 0;
+                }
+                if (ok && elect_one()) {
+                    if (kPair) tc::tc_commit2_mc(&tfull[a0], 0x3);
+                    else tc_commit(&tfull[a0]);
+                }
+                __syncwarp();
+            }
             if (!ok) {   // wait (bounded) for the MMAs already issued before TMEM is freed
-                if (kPair) tc::tc_commit2(drain);
-                else tc_commit(drain);
+                if (elect_one()) {
+                    if (kPair) tc::tc_commit2(drain);
+                    else tc_commit(drain);
+                }
+                __syncwarp();
                 mbar_wait(drain, 0, p.timeout_ns);
             }
         }
@@ -330,23 +404,24 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const CUtensorMa
             int it = 0;
             uint32_t raw_phase = 0;
             for (int i = first; i < total; i += step) {
-                const Tile t = tile_at<KIND, kPair>(p, s_off, s_cum, i);
+                const Tile t = tile(i);
                 const int nkb = (t.nc + kSl - 1) / kSl, left = t.nc % kSl;
                 it += nkb;
                 if (left == 0) continue;
                 const int stage = (it - 1) % kStages;
                 if (!__all_sync(0xffffffffu, mbar_wait(&raw[stage], (raw_phase >> stage) & 1u, p.timeout_ns))) break;
                 raw_phase ^= 1u << stage;
-                const int n16 = (kSl - left) * 8;   // 16-byte pieces of the cleared rows in each box
+                const int n16 = (kSl - left) * 8;   // 16-byte pieces of the cleared rows in each chunk of 64 values
                 for (int b = 0; b < 4; ++b) {
-                    uint4 *q = reinterpret_cast<uint4 *>((b < 2 ? sM : sN) + stage * kOpBytes + (b & 1) * 8192) + left * 8;
+                    uint4 *q = reinterpret_cast<uint4 *>((b < 2 ? sM : sN) + stage * kOpBytes + (b & 1) * (kOpBytes / 2)) +
+                               left * 8;
                     for (int j = lane; j < n16; j += 32) q[j] = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    if (kPair) tc::mbar_arrive_remote(tc::mapa_shared(smem_u32(&full[stage]), 0));
-                    else mbar_arrive(&full[stage]);
+                    if (kPair) tc::mbar_arrive_remote(tc::mapa_shared(smem_u32(&fixed[stage]), 0));
+                    else mbar_arrive(&fixed[stage]);
                 }
             }
         }
@@ -355,7 +430,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const CUtensorMa
         const int q = warp & 3, part = warp >> 2;
         int local = 0;
         for (int i = first; i < total; i += step) {
-            const Tile t = tile_at<KIND, kPair>(p, s_off, s_cum, i);
+            const Tile t = tile(i);
             if (t.rows <= 0) continue;
             const int f = t.f0 + (int)rank * 128 + q * 32 + lane;
             const bool f_ok = f < (KIND == NT ? p.n : p.k);
@@ -365,24 +440,28 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const CUtensorMa
                     for (int j = part; j < t.rows; j += 2) out[j * p.ldc + f] = TO(0.0f);
                 continue;
             }
-            const int a = local & 1;
-            const uint32_t aph = (local >> 1) & 1;
+            const int a0 = kWide ? 0 : local & 1;
+            const uint32_t ph = kWide ? local & 1 : (local >> 1) & 1;
             ++local;
             // warp-uniform decision: the TMEM loads below are warp-collective
-            if (!__all_sync(0xffffffffu, mbar_wait(&tfull[a], aph, p.timeout_ns))) break;
+            if (!__all_sync(0xffffffffu, mbar_wait(&tfull[a0], ph, p.timeout_ns))) break;
             tc_fence_after();
-            const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * kAccCols;
-            for (int c = part * 32; c < t.rows; c += 64) {
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(tb + c, r);
-                tmem_ld_wait();
-                store_cols(out + c * p.ldc, p.ldc, f, f_ok, r, t.rows - c, KIND == TN ? p.accumulate : 0);
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (kPair) tc::mbar_arrive_remote(tc::mapa_shared(smem_u32(&tempty[a]), 0));
-                else mbar_arrive(&tempty[a]);
+            for (int h = 0; h < t.nsub; ++h) {
+                const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (a0 + h) * kAccCols;
+                const int rows = min(t.nh, t.rows - h * t.nh);
+                TO *dst = out + (int64_t)h * t.nh * p.ldc;
+                for (int c = part * 32; c < rows; c += 64) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(tb + c, r);
+                    tmem_ld_wait();
+                    store_cols(dst + c * p.ldc, p.ldc, f, f_ok, r, rows - c, KIND == TN ? p.accumulate : 0);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (kPair) mbar_arrive_remote_relaxed(tc::mapa_shared(smem_u32(&tempty[a0 + h]), 0));
+                    else mbar_arrive(&tempty[a0 + h]);
+                }
             }
         }
     }
@@ -396,15 +475,15 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const CUtensorMa
     }
 }
 
-template <int KIND, typename TO>
+template <int KIND, typename TO, bool kWide>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
-    tc_pair_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_constant__ CUtensorMap tmN, const Params p) {
-    tc_body<KIND, TO, true>(tmM, tmN, p);
+    tc_pair_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_constant__ NMaps tmN, const Params p) {
+    tc_body<KIND, TO, true, kWide>(tmM, tmN, p);
 }
 template <int KIND, typename TO>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    tc_single_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_constant__ CUtensorMap tmN, const Params p) {
-    tc_body<KIND, TO, false>(tmM, tmN, p);
+    tc_single_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_constant__ NMaps tmN, const Params p) {
+    tc_body<KIND, TO, false, false>(tmM, tmN, p);
 }
 
 }  // namespace gmm
