@@ -150,24 +150,6 @@ int launch_gmm(const moe_gmm *d, const gmm::Params &p, const DeviceInfo &dev, cu
     return launch_gmm_tc<KIND, __nv_bfloat16>(p, dev, s);
 }
 
-// Attributes of this file's kernels, set once per device with the others'.
-int expert_ops_attrs() {
-#define MOE_GMM_ATTR(KIND)                                                     \
-    MOE_TRY(allow_smem(gmm::tc_pair_kernel<KIND, float, false>));              \
-    MOE_TRY(allow_smem(gmm::tc_single_kernel<KIND, float>));                   \
-    MOE_TRY(allow_smem(gmm::tc_pair_kernel<KIND, __nv_bfloat16, false>));      \
-    MOE_TRY(allow_smem(gmm::tc_single_kernel<KIND, __nv_bfloat16>))
-    MOE_GMM_ATTR(gmm::NT);
-    MOE_GMM_ATTR(gmm::NN);
-    MOE_GMM_ATTR(gmm::TN);
-    MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NT, float, true>));
-    MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NT, __nv_bfloat16, true>));
-    MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NN, float, true>));
-    MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NN, __nv_bfloat16, true>));
-#undef MOE_GMM_ATTR
-    return MOE_OK;
-}
-
 // ---------------------------------------------------------------- 8-bit checkpoints
 int make_ckpt_params(const moe_ckpt *d, int64_t rows, ckpt::Params *p) {
     if (!d || rows < 0 || rows > INT32_MAX) return MOE_ERR_INVALID_ARG;
@@ -218,6 +200,7 @@ int make_q4_params(const moe_q4 *d, q4::Params *p) {
     if (d->format == MOE_Q4_E2M1 && d->group != 32) return MOE_ERR_UNSUPPORTED;
     if (d->n < 1 || d->n % 8 || (d->act == MOE_ACT_SWIGLU && d->n % 16)) return MOE_ERR_INVALID_ARG;
     if (d->k < 1 || d->k % 32 || d->n > (1 << 20) || d->k > (1 << 20)) return MOE_ERR_INVALID_ARG;
+    if ((int64_t)d->experts * d->n > INT32_MAX) return MOE_ERR_UNSUPPORTED;   // rows are tensor-map coordinates
     *p = q4::Params{};
     p->N = d->experts;
     p->n = d->n;
@@ -227,21 +210,69 @@ int make_q4_params(const moe_q4 *d, q4::Params *p) {
     return MOE_OK;
 }
 
-template <int FMT, int ACT>
-int launch_q4(const q4::Params &p, int y_dtype, cudaStream_t s) {
-    const int cols = ACT == q4::SWIGLU ? p.n / 2 : p.n;
-    const dim3 grid((unsigned)cdiv(cols, q4::kThreads / 32), (unsigned)std::min<int64_t>(p.pairs, 65535));
-    if (y_dtype == MOE_F32) return launch_pdl(q4::matvec_kernel<FMT, ACT, float>, grid, dim3(q4::kThreads), 0, s, p);
-    return launch_pdl(q4::matvec_kernel<FMT, ACT, __nv_bfloat16>, grid, dim3(q4::kThreads), 0, s, p);
-}
-template <int FMT>
-int launch_q4_act(int act, const q4::Params &p, int y_dtype, cudaStream_t s) {
-    if (act == MOE_ACT_GELU) return launch_q4<FMT, q4::GELU>(p, y_dtype, s);
-    if (act == MOE_ACT_SWIGLU) return launch_q4<FMT, q4::SWIGLU>(p, y_dtype, s);
-    return launch_q4<FMT, q4::NONE>(p, y_dtype, s);
+// Codes [rows, k / 2] as boxes of 8 rows x 128 bytes, 128-byte swizzle.
+int make_map_codes(CUtensorMap *m, const uint8_t *codes, int64_t rows, int64_t row_bytes) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return MOE_ERR_CUDA;
+    const cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)row_bytes};
+    const cuuint32_t box[2] = {128u, 8u}, estr[2] = {1u, 1u};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(codes), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
 }
 
-constexpr int64_t kQ4MaxPairs = 4096;
+template <int FMT, int ACT>
+int launch_q4(const q4::MatvecParams &p, int y_dtype, const DeviceInfo &dev, cudaStream_t s) {
+    CUtensorMap map;
+    MOE_TRY(make_map_codes(&map, p.codes, (int64_t)p.N * p.n, p.k / 2));
+    const int64_t live = std::min<int64_t>(p.N, p.pairs);
+    q4::MatvecParams q = p;
+    q.tiles = (int)(ACT == q4::SWIGLU ? p.n / 16 : cdiv(p.n, 16));
+    // split k over warps while one round of blocks (20 warps per SM) has room: with few tiles more rows stream at once
+    q.ks = 1;
+    while (q.ks < q4::kWarps && live * q.tiles * q.ks * 2 <= (int64_t)dev.sms * 20 && q.ks * 2 * q4::kChunk <= p.k)
+        q.ks *= 2;
+    const dim3 grid((unsigned)cdiv(q.tiles, q4::kWarps / q.ks), (unsigned)live);
+    const size_t smem = q4::matvec_smem(p.pairs);
+    const dim3 block(q4::kWarps * 32);
+    if (y_dtype == MOE_F32) return launch_pdl(q4::matvec_kernel<FMT, ACT, float>, grid, block, smem, s, map, q);
+    return launch_pdl(q4::matvec_kernel<FMT, ACT, __nv_bfloat16>, grid, block, smem, s, map, q);
+}
+template <int FMT>
+int launch_q4_act(int act, const q4::MatvecParams &p, int y_dtype, const DeviceInfo &dev, cudaStream_t s) {
+    if (act == MOE_ACT_GELU) return launch_q4<FMT, q4::GELU>(p, y_dtype, dev, s);
+    if (act == MOE_ACT_SWIGLU) return launch_q4<FMT, q4::SWIGLU>(p, y_dtype, dev, s);
+    return launch_q4<FMT, q4::NONE>(p, y_dtype, dev, s);
+}
+
+// Attributes of this file's kernels, set once per device with the others'.
+int expert_ops_attrs() {
+#define MOE_GMM_ATTR(KIND)                                                     \
+    MOE_TRY(allow_smem(gmm::tc_pair_kernel<KIND, float, false>));              \
+    MOE_TRY(allow_smem(gmm::tc_single_kernel<KIND, float>));                   \
+    MOE_TRY(allow_smem(gmm::tc_pair_kernel<KIND, __nv_bfloat16, false>));      \
+    MOE_TRY(allow_smem(gmm::tc_single_kernel<KIND, __nv_bfloat16>))
+    MOE_GMM_ATTR(gmm::NT);
+    MOE_GMM_ATTR(gmm::NN);
+    MOE_GMM_ATTR(gmm::TN);
+    MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NT, float, true>));
+    MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NT, __nv_bfloat16, true>));
+    MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NN, float, true>));
+    MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NN, __nv_bfloat16, true>));
+#undef MOE_GMM_ATTR
+#define MOE_Q4_ATTR(FMT, ACT)                                       \
+    MOE_TRY(allow_smem(q4::matvec_kernel<FMT, ACT, float>));        \
+    MOE_TRY(allow_smem(q4::matvec_kernel<FMT, ACT, __nv_bfloat16>))
+    MOE_Q4_ATTR(q4::INT4, q4::NONE);
+    MOE_Q4_ATTR(q4::INT4, q4::GELU);
+    MOE_Q4_ATTR(q4::INT4, q4::SWIGLU);
+    MOE_Q4_ATTR(q4::E2M1, q4::NONE);
+    MOE_Q4_ATTR(q4::E2M1, q4::GELU);
+    MOE_Q4_ATTR(q4::E2M1, q4::SWIGLU);
+#undef MOE_Q4_ATTR
+    return MOE_OK;
+}
 
 }  // namespace
 
@@ -386,10 +417,10 @@ int moe_q4_dequantize(const moe_q4 *d, const uint8_t *codes, const void *scales,
 int moe_q4_matvec(const moe_q4 *d, const void *x, int64_t pairs, int32_t x_div, const int32_t *expert,
                   const uint8_t *codes, const void *scales, const float *gate, void *y, int32_t y_dtype,
                   moe_stream_t stream) {
-    q4::Params p;
+    q4::MatvecParams p{};
     MOE_TRY(make_q4_params(d, &p));
     if (pairs < 0 || x_div < 1 || !dtype_ok(y_dtype)) return MOE_ERR_INVALID_ARG;
-    if (pairs > kQ4MaxPairs) return MOE_ERR_UNSUPPORTED;
+    if (pairs > q4::kMaxPairs) return MOE_ERR_UNSUPPORTED;
     if (pairs == 0) return MOE_OK;
     if (!x || !expert || !codes || !scales || !y) return MOE_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) || !aligned16(y) || !aligned4(expert) || !aligned4(gate))
@@ -402,9 +433,12 @@ int moe_q4_matvec(const moe_q4 *d, const void *x, int64_t pairs, int32_t x_div, 
     p.scales = scales;
     p.gate = gate;
     p.y = y;
+    p.timeout_ns = kTimeoutNs;
+    DeviceInfo *dev = nullptr;
+    MOE_TRY(device_info(&dev));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (d->format == MOE_Q4_INT4) return launch_q4_act<q4::INT4>(d->act, p, y_dtype, s);
-    return launch_q4_act<q4::E2M1>(d->act, p, y_dtype, s);
+    if (d->format == MOE_Q4_INT4) return launch_q4_act<q4::INT4>(d->act, p, y_dtype, *dev, s);
+    return launch_q4_act<q4::E2M1>(d->act, p, y_dtype, *dev, s);
 }
 
 }  // extern "C"

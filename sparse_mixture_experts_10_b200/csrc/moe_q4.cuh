@@ -48,53 +48,302 @@ __device__ __forceinline__ float scale_of(const void *s, int64_t i) {
 __device__ __forceinline__ float gelu(float v) { return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f)); }
 __device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
 
+// ---------------------------------------------------------------- the products
+// One warp per 16 rows of W[e] (SwiGLU: 8 gate rows and the 8 up rows beside
+// them, so that a lane ends with both) and per share of k, against up to 32
+// pairs of the expert as columns of m16n8k16 products (bf16 x bf16 -> fp32).
+// A code is at most 4 bits, exact in bf16; the products of a group of 32 are
+// summed in fp32 by the tensor core and enter the result with one fp32
+// multiply-add by the group's scale, so nothing is rounded to fewer bits before
+// the end.
+//
+// Bound by HBM (0.5 byte per weight).  Each warp streams its 16 rows itself, as
+// boxes of 16 x 128 bytes (256 values of k) into a ring of its own: no block
+// barrier in the loop, and 5 boxes x 20 warps = 200 KB per SM in flight.  The
+// 128-byte swizzle lets the fragment reads (4 bytes per lane: 8 rows x 16
+// bytes) hit 32 different banks.  Inside a group the order of k is free: lane t
+// of a row takes the 8 codes of one 32-bit word, as pairs (i, i + 4) that one
+// mask each extracts, and x is permuted the same way.
+constexpr int kWarps = 4, kSlots = 5, kBoxBytes = 2048, kChunk = 256;
+constexpr int kMaxPairs = 4096, kMaxExperts = 1024;
+
+struct MatvecParams : Params {
+    int tiles, ks;         // 16-row tiles of an expert; warps of a block that share a tile (split k)
+    uint64_t timeout_ns;
+};
+
+// 8 codes as four bf16 pairs (i, i + 4), i = 0..3.
 template <int FMT>
-__device__ __forceinline__ float row_dot(const Params &p, int64_t row, const __nv_bfloat16 *x) {
-    const int lane = threadIdx.x & 31;
-    float sum = 0.f;
-    for (int j = lane * 8; j < p.k; j += 256) {   // 8 codes: inside one group
-        const uint32_t c = *reinterpret_cast<const uint32_t *>(p.codes + row * (p.k / 2) + j / 2);
-        const uint4 xv = *reinterpret_cast<const uint4 *>(x + j);
-        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-        float part = 0.f;
+__device__ __forceinline__ void decode8(uint32_t w, uint32_t (&v)[4]) {
+    if (FMT == INT4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {   // 0x4300 | c is 128 + c; minus 136 exactly c - 8
+            uint32_t u = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+            asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(u) : "r"(0x43084308u));
+            v[i] = u;
+        }
+    } else {
+        // exponent and mantissa bits at bf16's place read as value 2^-126 (subnormals included); times 2^126 exactly
+        const uint32_t m[4] = {w << 6, w << 2, w >> 2, w >> 6}, s[4] = {w << 12, w << 8, w << 4, w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            part = fmaf(code_value<FMT>((c >> (8 * i)) & 15u), __uint_as_float(xw[i] << 16), part);
-            part = fmaf(code_value<FMT>((c >> (8 * i + 4)) & 15u), __uint_as_float(xw[i] & 0xffff0000u), part);
+            uint32_t u = (m[i] & 0x01c001c0u) | (s[i] & 0x80008000u);
+            asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(u) : "r"(0x7e807e80u));
+            v[i] = u;
         }
-        sum = fmaf(part, scale_of<FMT>(p.scales, row * p.groups + (j >> p.group_shift)), sum);
     }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum;
 }
 
-// One warp per result of a pair.
-template <int FMT, int ACT, typename TO>
-__global__ void __launch_bounds__(kThreads) matvec_kernel(const Params p) {
-    pdl_enter();
-    const int cols = ACT == SWIGLU ? p.n / 2 : p.n;
-    const int i = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    if (i >= cols) return;
-    for (int64_t pr = blockIdx.y; pr < p.pairs; pr += gridDim.y) {
-        const int e = p.expert[pr];
-        float v = 0.f;
-        if (e >= 0 && e < p.N) {
-            const __nv_bfloat16 *x = p.x + pr / p.x_div * p.k;
-            v = row_dot<FMT>(p, (int64_t)e * p.n + i, x);
-            if (ACT == SWIGLU) v = silu(v) * row_dot<FMT>(p, (int64_t)e * p.n + cols + i, x);
-            if (ACT == GELU) v = gelu(v);
-            if (p.gate) v *= p.gate[pr];
-        } else if (e != -1 && (threadIdx.x & 31) == 0) {
-            set_status(kStatusBounds);
-        }
-        if ((threadIdx.x & 31) == 0) {
-            TO *y = static_cast<TO *>(p.y) + pr * cols + i;
-            if (sizeof(TO) == 4) *reinterpret_cast<float *>(y) = v;
-            else *reinterpret_cast<__nv_bfloat16 *>(y) = __float2bfloat16(v);
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Scales of the rows g and g + 8 for the 32-value pieces 2t and 2t + 1 of a chunk of k (0 past the end).
+template <int FMT>
+struct Scales {
+    float v[4];
+    __device__ __forceinline__ void load(const MatvecParams &p, int64_t row0, int64_t row1, int chunk, int t) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int k0 = chunk * kChunk + (2 * t + j) * 32;
+            const bool in = k0 < p.k;
+            v[j] = in && row0 >= 0 ? scale_of<FMT>(p.scales, row0 * p.groups + (k0 >> p.group_shift)) : 0.f;
+            v[2 + j] = in && row1 >= 0 ? scale_of<FMT>(p.scales, row1 * p.groups + (k0 >> p.group_shift)) : 0.f;
         }
     }
+};
+
+// One warp's share of k against columns col0.. of the expert's pairs (NB blocks of 8).
+// acc[b]: rows g (0, 1) and g + 8 (2, 3), columns 2t and 2t + 1.  False if a wait ran out.
+template <int FMT, int NB>
+__device__ __forceinline__ bool stream_rows(const MatvecParams &p, const CUtensorMap *map, uint8_t *ring, uint64_t *bars,
+                                            uint32_t &phases, bool swiglu, int box_row0, int box_row1, int64_t row0,
+                                            int64_t row1, int c_lo, int c_hi, const uint16_t *list, int cnt,
+                                            float (&acc)[NB][4]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int n = c_hi - c_lo;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[b][i] = 0.f;
+    if (n <= 0) return true;
+    auto issue = [&](int i) {   // box i of this share into slot i % kSlots
+        const int slot = i % kSlots;
+        mbar_arrive_expect_tx(&bars[slot], kBoxBytes);
+        tma_load_2d(map, &bars[slot], ring + slot * kBoxBytes, (c_lo + i) * (kChunk / 2), box_row0);
+        tma_load_2d(map, &bars[slot], ring + slot * kBoxBytes + 1024, (c_lo + i) * (kChunk / 2), box_row1);
+    };
+    if (lane == 0)
+        for (int i = 0; i < min(n, kSlots); ++i) issue(i);
+    Scales<FMT> s0, s1, s2;   // three chunks ahead: the scales come straight from global memory
+    s0.load(p, row0, row1, c_lo, t);
+    if (n > 1) s1.load(p, row0, row1, c_lo + 1, t);
+    if (n > 2) s2.load(p, row0, row1, c_lo + 2, t);
+    const __nv_bfloat16 *xr[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int col = b * 8 + g;
+        xr[b] = col < cnt ? p.x + (int64_t)(list[col] / p.x_div) * p.k + t * 8 : nullptr;
+    }
+    int slot = 0;
+    for (int i = 0; i < n; ++i) {
+        const int k0 = (c_lo + i) * kChunk;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars[slot], (phases >> slot) & 1u, p.timeout_ns))) {
+            if (lane == 0)   // copies still in flight land before the block leaves
+                for (int j = i; j < min(n, i + kSlots); ++j)
+                    mbar_wait(&bars[j % kSlots], (phases >> (j % kSlots)) & 1u, p.timeout_ns);
+            return false;
+        }
+        phases ^= 1u << slot;
+        const uint8_t *box = ring + slot * kBoxBytes + g * 128 + t * 4;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const uint32_t off = (uint32_t)((c ^ g) << 4);
+            uint32_t lo[4], hi[4];
+            decode8<FMT>(*reinterpret_cast<const uint32_t *>(box + off), lo);
+            decode8<FMT>(*reinterpret_cast<const uint32_t *>(box + 1024 + off), hi);
+            const float sa = __shfl_sync(0xffffffffu, s0.v[c & 1], (lane & ~3) | (c >> 1));
+            const float sb = __shfl_sync(0xffffffffu, s0.v[2 + (c & 1)], (lane & ~3) | (c >> 1));
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                uint4 xv = make_uint4(0, 0, 0, 0);
+                if (xr[b] && k0 + c * 32 < p.k) xv = __ldg(reinterpret_cast<const uint4 *>(xr[b] + k0 + c * 32));
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                mma16816(d, lo[0], hi[0], lo[1], hi[1], __byte_perm(xv.x, xv.z, 0x5410), __byte_perm(xv.x, xv.z, 0x7632));
+                mma16816(d, lo[2], hi[2], lo[3], hi[3], __byte_perm(xv.y, xv.w, 0x5410), __byte_perm(xv.y, xv.w, 0x7632));
+                acc[b][0] = fmaf(sa, d[0], acc[b][0]);
+                acc[b][1] = fmaf(sa, d[1], acc[b][1]);
+                acc[b][2] = fmaf(sb, d[2], acc[b][2]);
+                acc[b][3] = fmaf(sb, d[3], acc[b][3]);
+            }
+        }
+        __syncwarp();
+        if (lane == 0 && i + kSlots < n) issue(i + kSlots);
+        s0 = s1;
+        s1 = s2;
+        if (i + 3 < n) s2.load(p, row0, row1, c_lo + i + 3, t);
+        if (++slot == kSlots) slot = 0;
+    }
+    return true;
 }
+
+template <typename TO>
+__device__ __forceinline__ void put(TO *p, float v);
+template <>
+__device__ __forceinline__ void put<float>(float *p, float v) { *p = v; }
+template <>
+__device__ __forceinline__ void put<__nv_bfloat16>(__nv_bfloat16 *p, float v) { *p = __float2bfloat16(v); }
+
+// The expert's pairs list[0..cnt), at most 8 NB of them.
+template <int FMT, int ACT, typename TO, int NB>
+__device__ __forceinline__ bool tile_columns(const MatvecParams &p, const CUtensorMap *map, uint8_t *ring, uint64_t *bars,
+                                             uint32_t &phases, float (*part)[NB * 4][32], int e, int tile,
+                                             const uint16_t *list, int cnt) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int share = warp % p.ks, cols = ACT == SWIGLU ? p.n / 2 : p.n;
+    const int i0 = tile * (ACT == SWIGLU ? 8 : 16);
+    const int64_t base = (int64_t)e * p.n;
+    const int r0 = i0 + g, r1 = ACT == SWIGLU ? cols + i0 + g : i0 + 8 + g;   // this lane's two rows
+    const int chunks = (p.k + kChunk - 1) / kChunk;
+    float acc[NB][4];
+    bool ok = true;
+    if (tile < p.tiles) {
+        ok = stream_rows<FMT, NB>(p, map, ring, bars, phases, ACT == SWIGLU, (int)(base + i0),
+                                  (int)(base + (ACT == SWIGLU ? cols + i0 : i0 + 8)), base + r0,
+                                  r1 < p.n ? base + r1 : -1, chunks * share / p.ks, chunks * (share + 1) / p.ks, list, cnt,
+                                  acc);
+    }
+    if (p.ks > 1) {   // the shares of k are added in their order
+        if (share > 0)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) part[warp][b * 4 + i][lane] = acc[b][i];
+        __syncthreads();
+        if (share == 0)
+            for (int s = 1; s < p.ks; ++s)
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[b][i] += part[warp + s][b * 4 + i][lane];
+        __syncthreads();
+    }
+    if (!ok || share > 0 || tile >= p.tiles) return ok;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int col = b * 8 + 2 * t + j;
+            if (col >= cnt) continue;
+            const int pr = list[col];
+            const float w = p.gate ? p.gate[pr] : 1.0f;
+            TO *y = static_cast<TO *>(p.y) + (int64_t)pr * cols;
+            const float v0 = acc[b][j], v1 = acc[b][2 + j];
+            if (ACT == SWIGLU) {
+                put(y + r0, w * (silu(v0) * v1));
+            } else {
+                put(y + r0, w * (ACT == GELU ? gelu(v0) : v0));
+                if (r1 < p.n) put(y + r1, w * (ACT == GELU ? gelu(v1) : v1));
+            }
+        }
+    return ok;
+}
+
+// Grid (tile groups, live experts at most): block (x, y) takes kWarps / ks tiles of the y-th expert that has a pair.
+template <int FMT, int ACT, typename TO>
+__global__ void __launch_bounds__(kWarps * 32, 4)
+    matvec_kernel(const __grid_constant__ CUtensorMap map, const MatvecParams p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = align_smem_1024(smem_raw);
+    __shared__ uint64_t s_bar[kWarps][kSlots];
+    __shared__ uint32_t s_mask[kMaxExperts / 32];
+    __shared__ int s_e, s_cnt, s_bad;
+    __shared__ float s_part[kWarps][16][32];
+    uint16_t *s_list = reinterpret_cast<uint16_t *>(smem + kWarps * kSlots * kBoxBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x < kWarps * kSlots) mbar_init(&s_bar[threadIdx.x / kSlots][threadIdx.x % kSlots], 1);
+    fence_mbar_init();
+    if (threadIdx.x < kMaxExperts / 32) s_mask[threadIdx.x] = 0;
+    if (threadIdx.x == 0) {
+        s_e = -1;
+        s_bad = 0;
+        tma_prefetch_desc(&map);
+    }
+    __syncthreads();
+    pdl_enter();
+    const int pairs = (int)p.pairs;
+    for (int i = threadIdx.x; i < pairs; i += kWarps * 32) {
+        const int e = p.expert[i];
+        if (e >= 0 && e < p.N) atomicOr(&s_mask[e >> 5], 1u << (e & 31));
+        else s_bad = 1;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const uint32_t m = s_mask[lane];
+        int incl = __popc(m);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        const int want = (int)blockIdx.y - (incl - __popc(m));   // this word's want-th live expert
+        if (want >= 0 && want < __popc(m)) {
+            uint32_t r = m;
+            for (int i = 0; i < want; ++i) r &= r - 1;
+            s_e = lane * 32 + __ffs(r) - 1;
+        }
+        __syncwarp();
+        const int e = *(volatile int *)&s_e;
+        int cnt = 0;
+        if (e >= 0)
+            for (int i0 = 0; i0 < pairs; i0 += 32) {   // the expert's pairs in order
+                const bool mine = i0 + lane < pairs && p.expert[i0 + lane] == e;
+                const uint32_t b = __ballot_sync(0xffffffffu, mine);
+                if (mine) s_list[cnt + __popc(b & ((1u << lane) - 1))] = (uint16_t)(i0 + lane);
+                cnt += __popc(b);
+            }
+        if (lane == 0) s_cnt = cnt;
+    }
+    __syncthreads();
+    const int tiles_here = kWarps / p.ks, tile = blockIdx.x * tiles_here + warp / p.ks;
+    if (s_bad && blockIdx.y == 0) {   // rows of pairs without an expert
+        const int cols = ACT == SWIGLU ? p.n / 2 : p.n, per = (ACT == SWIGLU ? 8 : 16) * tiles_here;
+        const int c0 = blockIdx.x * per, c1 = min(c0 + per, cols);
+        for (int i = 0; i < pairs; ++i) {
+            const int e = p.expert[i];
+            if (e >= 0 && e < p.N) continue;
+            if (e != -1 && blockIdx.x == 0 && threadIdx.x == 0) set_status(kStatusBounds);
+            for (int c = c0 + threadIdx.x; c < c1; c += kWarps * 32) put(static_cast<TO *>(p.y) + (int64_t)i * cols + c, 0.f);
+        }
+    }
+    const int e = s_e;
+    if (e < 0) return;
+    uint8_t *ring = smem + warp * kSlots * kBoxBytes;
+    uint32_t phases = 0;
+    // blocks of up to 32 pairs; the weights are read again for each
+    for (int c = 0; c < s_cnt; c += 32) {
+        const int left = s_cnt - c;
+        bool ok;
+        if (left <= 8)
+            ok = tile_columns<FMT, ACT, TO, 1>(p, &map, ring, s_bar[warp], phases,
+                                               reinterpret_cast<float(*)[4][32]>(s_part), e, tile, s_list + c, left);
+        else if (left <= 16)
+            ok = tile_columns<FMT, ACT, TO, 2>(p, &map, ring, s_bar[warp], phases,
+                                               reinterpret_cast<float(*)[8][32]>(s_part), e, tile, s_list + c, left);
+        else
+            ok = tile_columns<FMT, ACT, TO, 4>(p, &map, ring, s_bar[warp], phases,
+                                               reinterpret_cast<float(*)[16][32]>(s_part), e, tile, s_list + c,
+                                               min(left, 32));
+        if (!__syncthreads_and(ok)) return;   // a wait ran out (status word); nothing is in flight any more
+    }
+}
+
+constexpr size_t matvec_smem(int64_t pairs) { return 1024 + (size_t)kWarps * kSlots * kBoxBytes + (size_t)pairs * 2; }
 
 // Codes and scales of fp32 or bf16 weights: one warp per group of values.
 //   int4  s = bf16(max|w| / 7), code = 8 + round(w / s) clamped to 0..15
