@@ -222,28 +222,22 @@ int make_map_codes(CUtensorMap *m, const uint8_t *codes, int64_t rows, int64_t r
     return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
 }
 
-template <int FMT, int ACT>
-int launch_q4(const q4::MatvecParams &p, int y_dtype, const DeviceInfo &dev, cudaStream_t s) {
+int launch_q4(int format, const q4::MatvecParams &p, const DeviceInfo &dev, cudaStream_t s) {
     CUtensorMap map;
     MOE_TRY(make_map_codes(&map, p.codes, (int64_t)p.N * p.n, p.k / 2));
     const int64_t live = std::min<int64_t>(p.N, p.pairs);
     q4::MatvecParams q = p;
-    q.tiles = (int)(ACT == q4::SWIGLU ? p.n / 16 : cdiv(p.n, 16));
-    // split k over warps while one round of blocks (20 warps per SM) has room: with few tiles more rows stream at once
+    q.tiles = (int)cdiv(p.n, 16);
+    // split k over warps while one round of blocks (16 warps per SM) has room: with few tiles more rows stream at once
     q.ks = 1;
-    while (q.ks < q4::kWarps && live * q.tiles * q.ks * 2 <= (int64_t)dev.sms * 20 && q.ks * 2 * q4::kChunk <= p.k)
+    while (q.ks < q4::kWarps && live * q.tiles * q.ks * 2 <= (int64_t)dev.sms * 16 && q.ks * 2 * q4::kChunk <= p.k)
         q.ks *= 2;
     const dim3 grid((unsigned)cdiv(q.tiles, q4::kWarps / q.ks), (unsigned)live);
-    const size_t smem = q4::matvec_smem(p.pairs);
-    const dim3 block(q4::kWarps * 32);
-    if (y_dtype == MOE_F32) return launch_pdl(q4::matvec_kernel<FMT, ACT, float>, grid, block, smem, s, map, q);
-    return launch_pdl(q4::matvec_kernel<FMT, ACT, __nv_bfloat16>, grid, block, smem, s, map, q);
-}
-template <int FMT>
-int launch_q4_act(int act, const q4::MatvecParams &p, int y_dtype, const DeviceInfo &dev, cudaStream_t s) {
-    if (act == MOE_ACT_GELU) return launch_q4<FMT, q4::GELU>(p, y_dtype, dev, s);
-    if (act == MOE_ACT_SWIGLU) return launch_q4<FMT, q4::SWIGLU>(p, y_dtype, dev, s);
-    return launch_q4<FMT, q4::NONE>(p, y_dtype, dev, s);
+    auto *k = format == MOE_Q4_E2M1      ? q4::matvec_kernel<q4::E2M1, 5>
+              : p.group_shift == 5       ? q4::matvec_kernel<q4::INT4, 5>
+              : p.group_shift == 6       ? q4::matvec_kernel<q4::INT4, 6>
+                                         : q4::matvec_kernel<q4::INT4, 7>;
+    return launch_pdl(k, grid, dim3(q4::kWarps * 32), q4::matvec_smem(p.pairs), s, map, q);
 }
 
 // Attributes of this file's kernels, set once per device with the others'.
@@ -261,16 +255,10 @@ int expert_ops_attrs() {
     MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NN, float, true>));
     MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NN, __nv_bfloat16, true>));
 #undef MOE_GMM_ATTR
-#define MOE_Q4_ATTR(FMT, ACT)                                       \
-    MOE_TRY(allow_smem(q4::matvec_kernel<FMT, ACT, float>));        \
-    MOE_TRY(allow_smem(q4::matvec_kernel<FMT, ACT, __nv_bfloat16>))
-    MOE_Q4_ATTR(q4::INT4, q4::NONE);
-    MOE_Q4_ATTR(q4::INT4, q4::GELU);
-    MOE_Q4_ATTR(q4::INT4, q4::SWIGLU);
-    MOE_Q4_ATTR(q4::E2M1, q4::NONE);
-    MOE_Q4_ATTR(q4::E2M1, q4::GELU);
-    MOE_Q4_ATTR(q4::E2M1, q4::SWIGLU);
-#undef MOE_Q4_ATTR
+    MOE_TRY(allow_smem(q4::matvec_kernel<q4::INT4, 5>));
+    MOE_TRY(allow_smem(q4::matvec_kernel<q4::INT4, 6>));
+    MOE_TRY(allow_smem(q4::matvec_kernel<q4::INT4, 7>));
+    MOE_TRY(allow_smem(q4::matvec_kernel<q4::E2M1, 5>));
     return MOE_OK;
 }
 
@@ -437,8 +425,9 @@ int moe_q4_matvec(const moe_q4 *d, const void *x, int64_t pairs, int32_t x_div, 
     DeviceInfo *dev = nullptr;
     MOE_TRY(device_info(&dev));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (d->format == MOE_Q4_INT4) return launch_q4_act<q4::INT4>(d->act, p, y_dtype, *dev, s);
-    return launch_q4_act<q4::E2M1>(d->act, p, y_dtype, *dev, s);
+    p.act = d->act;
+    p.y_f32 = y_dtype == MOE_F32;
+    return launch_q4(d->format, p, *dev, s);
 }
 
 }  // extern "C"

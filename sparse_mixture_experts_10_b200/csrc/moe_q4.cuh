@@ -50,7 +50,7 @@ __device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
 
 // ---------------------------------------------------------------- the products
 // One warp per 16 rows of W[e] (SwiGLU: 8 gate rows and the 8 up rows beside
-// them, so that a lane ends with both) and per share of k, against up to 32
+// them, so that a lane ends with both) and per share of k, against up to 16
 // pairs of the expert as columns of m16n8k16 products (bf16 x bf16 -> fp32).
 // A code is at most 4 bits, exact in bf16; the products of a group of 32 are
 // summed in fp32 by the tensor core and enter the result with one fp32
@@ -59,7 +59,7 @@ __device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
 //
 // Bound by HBM (0.5 byte per weight).  Each warp streams its 16 rows itself, as
 // boxes of 16 x 128 bytes (256 values of k) into a ring of its own: no block
-// barrier in the loop, and 5 boxes x 20 warps = 200 KB per SM in flight.  The
+// barrier in the loop, and 5 boxes x 16 warps = 160 KB per SM in flight.  The
 // 128-byte swizzle lets the fragment reads (4 bytes per lane: 8 rows x 16
 // bytes) hit 32 different banks.  Inside a group the order of k is free: lane t
 // of a row takes the 8 codes of one 32-bit word, as pairs (i, i + 4) that one
@@ -68,6 +68,7 @@ constexpr int kWarps = 4, kSlots = 5, kBoxBytes = 2048, kChunk = 256;
 constexpr int kMaxPairs = 4096, kMaxExperts = 1024;
 
 struct MatvecParams : Params {
+    int act, y_f32;
     int tiles, ks;         // 16-row tiles of an expert; warps of a block that share a tile (split k)
     uint64_t timeout_ns;
 };
@@ -94,37 +95,63 @@ __device__ __forceinline__ void decode8(uint32_t w, uint32_t (&v)[4]) {
     }
 }
 
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+// d = A B (first) or d += A B
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, "
+        "%10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
         "%2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Scales of the rows g and g + 8 for the 32-value pieces 2t and 2t + 1 of a chunk of k (0 past the end).
-template <int FMT>
-struct Scales {
-    float v[4];
-    __device__ __forceinline__ void load(const MatvecParams &p, int64_t row0, int64_t row1, int chunk, int t) {
+// What a lane holds of a chunk of k: the scales of the rows g and g + 8 for the 32-value pieces 2t and 2t + 1
+// (one scale for both with groups of 64 and more; 0 past the last group).
+template <int FMT, int SHIFT>
+struct ScaleRows {
+    static constexpr int kN = SHIFT == 5 ? 2 : 1;
+    int64_t row0, row1;   // first scale of the row; row1 < 0: no such row
+    __device__ __forceinline__ void load(const MatvecParams &p, int chunk, int t, float (&v)[2 * kN]) const {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int k0 = chunk * kChunk + (2 * t + j) * 32;
-            const bool in = k0 < p.k;
-            v[j] = in && row0 >= 0 ? scale_of<FMT>(p.scales, row0 * p.groups + (k0 >> p.group_shift)) : 0.f;
-            v[2 + j] = in && row1 >= 0 ? scale_of<FMT>(p.scales, row1 * p.groups + (k0 >> p.group_shift)) : 0.f;
+        for (int j = 0; j < kN; ++j) {
+            const int at = (chunk * kChunk + (2 * t + j) * 32) >> SHIFT;
+            const bool in = at < p.groups;
+            v[j] = in ? scale_of<FMT>(p.scales, row0 + at) : 0.f;
+            v[kN + j] = in && row1 >= 0 ? scale_of<FMT>(p.scales, row1 + at) : 0.f;
         }
     }
 };
 
-// One warp's share of k against columns col0.. of the expert's pairs (NB blocks of 8).
+// x of the columns g (+ 8 b) for four pieces of k from k0: 8 values per lane and piece, 0 from k on.
+template <int NB>
+__device__ __forceinline__ void load_x(const __nv_bfloat16 *const (&xr)[NB], int k0, int k, uint4 (&v)[NB][4]) {
+    if (k0 + 128 <= k) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[b][c] = __ldg(reinterpret_cast<const uint4 *>(xr[b] + k0 + c * 32));
+    } else {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                v[b][c] = k0 + c * 32 < k ? __ldg(reinterpret_cast<const uint4 *>(xr[b] + k0 + c * 32))
+                                          : make_uint4(0, 0, 0, 0);
+    }
+}
+
+// One warp's share of k against columns of the expert's pairs (NB blocks of 8).
 // acc[b]: rows g (0, 1) and g + 8 (2, 3), columns 2t and 2t + 1.  False if a wait ran out.
-template <int FMT, int NB>
+template <int FMT, int SHIFT, int NB>
 __device__ __forceinline__ bool stream_rows(const MatvecParams &p, const CUtensorMap *map, uint8_t *ring, uint64_t *bars,
-                                            uint32_t &phases, bool swiglu, int box_row0, int box_row1, int64_t row0,
-                                            int64_t row1, int c_lo, int c_hi, const uint16_t *list, int cnt,
-                                            float (&acc)[NB][4]) {
+                                            uint32_t &phases, int box_row0, int box_row1, int64_t row0, int64_t row1,
+                                            int c_lo, int c_hi, const uint16_t *list, int cnt, float (&acc)[NB][4]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int n = c_hi - c_lo;
 #pragma unroll
@@ -132,27 +159,33 @@ __device__ __forceinline__ bool stream_rows(const MatvecParams &p, const CUtenso
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[b][i] = 0.f;
     if (n <= 0) return true;
-    auto issue = [&](int i) {   // box i of this share into slot i % kSlots
-        const int slot = i % kSlots;
+    auto issue = [&](int i, int slot) {   // box i of this share
         mbar_arrive_expect_tx(&bars[slot], kBoxBytes);
         tma_load_2d(map, &bars[slot], ring + slot * kBoxBytes, (c_lo + i) * (kChunk / 2), box_row0);
         tma_load_2d(map, &bars[slot], ring + slot * kBoxBytes + 1024, (c_lo + i) * (kChunk / 2), box_row1);
     };
     if (lane == 0)
-        for (int i = 0; i < min(n, kSlots); ++i) issue(i);
-    Scales<FMT> s0, s1, s2;   // three chunks ahead: the scales come straight from global memory
-    s0.load(p, row0, row1, c_lo, t);
-    if (n > 1) s1.load(p, row0, row1, c_lo + 1, t);
-    if (n > 2) s2.load(p, row0, row1, c_lo + 2, t);
+        for (int i = 0; i < min(n, kSlots); ++i) issue(i, i);
+    // scales three chunks ahead: they come straight from global memory
+    using Rows = ScaleRows<FMT, SHIFT>;
+    constexpr int kN = Rows::kN;
+    const Rows rows{row0 * p.groups, row1 < 0 ? -1 : row1 * p.groups};
+    float s0[2 * kN], s1[2 * kN] = {}, s2[2 * kN] = {};
+    rows.load(p, c_lo, t, s0);
+    if (n > 1) rows.load(p, c_lo + 1, t, s1);
+    if (n > 2) rows.load(p, c_lo + 2, t, s2);
+    // columns past the last pair repeat it; their results are not written
     const __nv_bfloat16 *xr[NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        const int col = b * 8 + g;
-        xr[b] = col < cnt ? p.x + (int64_t)(list[col] / p.x_div) * p.k + t * 8 : nullptr;
-    }
+    for (int b = 0; b < NB; ++b) xr[b] = p.x + (int64_t)(list[min(b * 8 + g, cnt - 1)] / p.x_div) * p.k + t * 8;
+    constexpr int kPieces = 1 << (SHIFT - 5);   // per scale: their products are added up before it is applied
+    // the word of piece c in the swizzled box: 16-byte unit c ^ g of row g; bits 4-6 of the rest are 0
+    const uint32_t at = (uint32_t)(g * 128 + t * 4 + (g << 4));
     int slot = 0;
     for (int i = 0; i < n; ++i) {
         const int k0 = (c_lo + i) * kChunk;
+        uint4 xa[NB][4], xb[NB][4];
+        load_x<NB>(xr, k0, p.k, xa);
         if (!__all_sync(0xffffffffu, mbar_wait(&bars[slot], (phases >> slot) & 1u, p.timeout_ns))) {
             if (lane == 0)   // copies still in flight land before the block leaves
                 for (int j = i; j < min(n, i + kSlots); ++j)
@@ -160,64 +193,66 @@ __device__ __forceinline__ bool stream_rows(const MatvecParams &p, const CUtenso
             return false;
         }
         phases ^= 1u << slot;
-        const uint8_t *box = ring + slot * kBoxBytes + g * 128 + t * 4;
+        load_x<NB>(xr, k0 + 128, p.k, xb);
+        const uint8_t *box = ring + slot * kBoxBytes;
+        float d[NB][4];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-            const uint32_t off = (uint32_t)((c ^ g) << 4);
+            const uint8_t *w = box + (at ^ (uint32_t)(c << 4));
             uint32_t lo[4], hi[4];
-            decode8<FMT>(*reinterpret_cast<const uint32_t *>(box + off), lo);
-            decode8<FMT>(*reinterpret_cast<const uint32_t *>(box + 1024 + off), hi);
-            const float sa = __shfl_sync(0xffffffffu, s0.v[c & 1], (lane & ~3) | (c >> 1));
-            const float sb = __shfl_sync(0xffffffffu, s0.v[2 + (c & 1)], (lane & ~3) | (c >> 1));
+            decode8<FMT>(*reinterpret_cast<const uint32_t *>(w), lo);
+            decode8<FMT>(*reinterpret_cast<const uint32_t *>(w + 1024), hi);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                uint4 xv = make_uint4(0, 0, 0, 0);
-                if (xr[b] && k0 + c * 32 < p.k) xv = __ldg(reinterpret_cast<const uint4 *>(xr[b] + k0 + c * 32));
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                mma16816(d, lo[0], hi[0], lo[1], hi[1], __byte_perm(xv.x, xv.z, 0x5410), __byte_perm(xv.x, xv.z, 0x7632));
-                mma16816(d, lo[2], hi[2], lo[3], hi[3], __byte_perm(xv.y, xv.w, 0x5410), __byte_perm(xv.y, xv.w, 0x7632));
-                acc[b][0] = fmaf(sa, d[0], acc[b][0]);
-                acc[b][1] = fmaf(sa, d[1], acc[b][1]);
-                acc[b][2] = fmaf(sb, d[2], acc[b][2]);
-                acc[b][3] = fmaf(sb, d[3], acc[b][3]);
+                const uint4 xv = c < 4 ? xa[b][c & 3] : xb[b][c & 3];
+                const uint32_t b0 = __byte_perm(xv.x, xv.z, 0x5410), b1 = __byte_perm(xv.x, xv.z, 0x7632);
+                const uint32_t b2 = __byte_perm(xv.y, xv.w, 0x5410), b3 = __byte_perm(xv.y, xv.w, 0x7632);
+                if (c % kPieces == 0) mma16816_first(d[b], lo[0], hi[0], lo[1], hi[1], b0, b1);
+                else mma16816(d[b], lo[0], hi[0], lo[1], hi[1], b0, b1);
+                mma16816(d[b], lo[2], hi[2], lo[3], hi[3], b2, b3);
+            }
+            if (c % kPieces == kPieces - 1) {
+                const float sa = __shfl_sync(0xffffffffu, s0[c % kN], (lane & ~3) | (c >> 1));
+                const float sb = __shfl_sync(0xffffffffu, s0[kN + c % kN], (lane & ~3) | (c >> 1));
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    acc[b][0] = fmaf(sa, d[b][0], acc[b][0]);
+                    acc[b][1] = fmaf(sa, d[b][1], acc[b][1]);
+                    acc[b][2] = fmaf(sb, d[b][2], acc[b][2]);
+                    acc[b][3] = fmaf(sb, d[b][3], acc[b][3]);
+                }
             }
         }
         __syncwarp();
-        if (lane == 0 && i + kSlots < n) issue(i + kSlots);
-        s0 = s1;
-        s1 = s2;
-        if (i + 3 < n) s2.load(p, row0, row1, c_lo + i + 3, t);
+        if (lane == 0 && i + kSlots < n) issue(i + kSlots, slot);
+#pragma unroll
+        for (int j = 0; j < 2 * kN; ++j) {
+            s0[j] = s1[j];
+            s1[j] = s2[j];
+        }
+        if (i + 3 < n) rows.load(p, c_lo + i + 3, t, s2);
         if (++slot == kSlots) slot = 0;
     }
     return true;
 }
 
-template <typename TO>
-__device__ __forceinline__ void put(TO *p, float v);
-template <>
-__device__ __forceinline__ void put<float>(float *p, float v) { *p = v; }
-template <>
-__device__ __forceinline__ void put<__nv_bfloat16>(__nv_bfloat16 *p, float v) { *p = __float2bfloat16(v); }
-
 // The expert's pairs list[0..cnt), at most 8 NB of them.
-template <int FMT, int ACT, typename TO, int NB>
+template <int FMT, int SHIFT, int NB>
 __device__ __forceinline__ bool tile_columns(const MatvecParams &p, const CUtensorMap *map, uint8_t *ring, uint64_t *bars,
                                              uint32_t &phases, float (*part)[NB * 4][32], int e, int tile,
                                              const uint16_t *list, int cnt) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int share = warp % p.ks, cols = ACT == SWIGLU ? p.n / 2 : p.n;
-    const int i0 = tile * (ACT == SWIGLU ? 8 : 16);
+    const bool swiglu = p.act == SWIGLU;
+    const int share = warp % p.ks, cols = swiglu ? p.n / 2 : p.n;
+    const int i0 = tile * (swiglu ? 8 : 16), i1 = swiglu ? cols + i0 : i0 + 8;   // first rows of the two halves
     const int64_t base = (int64_t)e * p.n;
-    const int r0 = i0 + g, r1 = ACT == SWIGLU ? cols + i0 + g : i0 + 8 + g;   // this lane's two rows
     const int chunks = (p.k + kChunk - 1) / kChunk;
     float acc[NB][4];
     bool ok = true;
-    if (tile < p.tiles) {
-        ok = stream_rows<FMT, NB>(p, map, ring, bars, phases, ACT == SWIGLU, (int)(base + i0),
-                                  (int)(base + (ACT == SWIGLU ? cols + i0 : i0 + 8)), base + r0,
-                                  r1 < p.n ? base + r1 : -1, chunks * share / p.ks, chunks * (share + 1) / p.ks, list, cnt,
-                                  acc);
-    }
+    if (tile < p.tiles)
+        ok = stream_rows<FMT, SHIFT, NB>(p, map, ring, bars, phases, (int)(base + i0), (int)(base + i1), base + i0 + g,
+                                         i1 + g < p.n ? base + i1 + g : -1, chunks * share / p.ks,
+                                         chunks * (share + 1) / p.ks, list, cnt, acc);
     if (p.ks > 1) {   // the shares of k are added in their order
         if (share > 0)
 #pragma unroll
@@ -234,6 +269,10 @@ __device__ __forceinline__ bool tile_columns(const MatvecParams &p, const CUtens
         __syncthreads();
     }
     if (!ok || share > 0 || tile >= p.tiles) return ok;
+    auto put = [&](int64_t at, float v) {
+        if (p.y_f32) static_cast<float *>(p.y)[at] = v;
+        else static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16(v);
+    };
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -242,20 +281,24 @@ __device__ __forceinline__ bool tile_columns(const MatvecParams &p, const CUtens
             if (col >= cnt) continue;
             const int pr = list[col];
             const float w = p.gate ? p.gate[pr] : 1.0f;
-            TO *y = static_cast<TO *>(p.y) + (int64_t)pr * cols;
-            const float v0 = acc[b][j], v1 = acc[b][2 + j];
-            if (ACT == SWIGLU) {
-                put(y + r0, w * (silu(v0) * v1));
+            const int64_t y = (int64_t)pr * cols + i0 + g;
+            float v0 = acc[b][j], v1 = acc[b][2 + j];
+            if (swiglu) {
+                put(y, w * (silu(v0) * v1));
             } else {
-                put(y + r0, w * (ACT == GELU ? gelu(v0) : v0));
-                if (r1 < p.n) put(y + r1, w * (ACT == GELU ? gelu(v1) : v1));
+                if (p.act == GELU) {
+                    v0 = gelu(v0);
+                    v1 = gelu(v1);
+                }
+                put(y, w * v0);
+                if (i1 + g < p.n) put(y + 8, w * v1);
             }
         }
     return ok;
 }
 
 // Grid (tile groups, live experts at most): block (x, y) takes kWarps / ks tiles of the y-th expert that has a pair.
-template <int FMT, int ACT, typename TO>
+template <int FMT, int SHIFT>
 __global__ void __launch_bounds__(kWarps * 32, 4)
     matvec_kernel(const __grid_constant__ CUtensorMap map, const MatvecParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -263,7 +306,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     __shared__ uint64_t s_bar[kWarps][kSlots];
     __shared__ uint32_t s_mask[kMaxExperts / 32];
     __shared__ int s_e, s_cnt, s_bad;
-    __shared__ float s_part[kWarps][16][32];
+    __shared__ float s_part[kWarps][8][32];
     uint16_t *s_list = reinterpret_cast<uint16_t *>(smem + kWarps * kSlots * kBoxBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x < kWarps * kSlots) mbar_init(&s_bar[threadIdx.x / kSlots][threadIdx.x % kSlots], 1);
@@ -312,33 +355,31 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     __syncthreads();
     const int tiles_here = kWarps / p.ks, tile = blockIdx.x * tiles_here + warp / p.ks;
     if (s_bad && blockIdx.y == 0) {   // rows of pairs without an expert
-        const int cols = ACT == SWIGLU ? p.n / 2 : p.n, per = (ACT == SWIGLU ? 8 : 16) * tiles_here;
+        const int cols = p.act == SWIGLU ? p.n / 2 : p.n, per = (p.act == SWIGLU ? 8 : 16) * tiles_here;
         const int c0 = blockIdx.x * per, c1 = min(c0 + per, cols);
         for (int i = 0; i < pairs; ++i) {
             const int e = p.expert[i];
             if (e >= 0 && e < p.N) continue;
             if (e != -1 && blockIdx.x == 0 && threadIdx.x == 0) set_status(kStatusBounds);
-            for (int c = c0 + threadIdx.x; c < c1; c += kWarps * 32) put(static_cast<TO *>(p.y) + (int64_t)i * cols + c, 0.f);
+            for (int c = c0 + threadIdx.x; c < c1; c += kWarps * 32) {
+                if (p.y_f32) static_cast<float *>(p.y)[(int64_t)i * cols + c] = 0.f;
+                else static_cast<__nv_bfloat16 *>(p.y)[(int64_t)i * cols + c] = __float2bfloat16(0.f);
+            }
         }
     }
     const int e = s_e;
     if (e < 0) return;
     uint8_t *ring = smem + warp * kSlots * kBoxBytes;
     uint32_t phases = 0;
-    // blocks of up to 32 pairs; the weights are read again for each
-    for (int c = 0; c < s_cnt; c += 32) {
+    // blocks of up to 16 pairs; the weights are read again (from L2) for each
+    for (int c = 0; c < s_cnt; c += 16) {
         const int left = s_cnt - c;
-        bool ok;
-        if (left <= 8)
-            ok = tile_columns<FMT, ACT, TO, 1>(p, &map, ring, s_bar[warp], phases,
-                                               reinterpret_cast<float(*)[4][32]>(s_part), e, tile, s_list + c, left);
-        else if (left <= 16)
-            ok = tile_columns<FMT, ACT, TO, 2>(p, &map, ring, s_bar[warp], phases,
-                                               reinterpret_cast<float(*)[8][32]>(s_part), e, tile, s_list + c, left);
-        else
-            ok = tile_columns<FMT, ACT, TO, 4>(p, &map, ring, s_bar[warp], phases,
-                                               reinterpret_cast<float(*)[16][32]>(s_part), e, tile, s_list + c,
-                                               min(left, 32));
+        const bool ok = left <= 8 ? tile_columns<FMT, SHIFT, 1>(p, &map, ring, s_bar[warp], phases,
+                                                                  reinterpret_cast<float(*)[4][32]>(s_part), e, tile,
+                                                                  s_list + c, left)
+                                  : tile_columns<FMT, SHIFT, 2>(p, &map, ring, s_bar[warp], phases,
+                                                                  reinterpret_cast<float(*)[8][32]>(s_part), e, tile,
+                                                                  s_list + c, min(left, 16));
         if (!__syncthreads_and(ok)) return;   // a wait ran out (status word); nothing is in flight any more
     }
 }
