@@ -475,7 +475,8 @@ enum { MOE_Q4_INT4 = 0, MOE_Q4_E2M1 = 1 };
 typedef struct {
     int32_t experts; /* 1..1024 */
     int32_t n;       /* rows of an expert's matrix: a multiple of 8 (SwiGLU: 16) */
-    int32_t k;       /* a multiple of 32 */
+    int32_t k;       /* a multiple of 32; moe_q4_matvec holds a row of x in shared
+                        memory: beyond about 50 thousand MOE_ERR_UNSUPPORTED */
     int32_t group;   /* values per scale */
     int32_t format;  /* MOE_Q4_* */
     int32_t act;     /* applied to the products: MOE_ACT_NONE, MOE_ACT_GELU, or

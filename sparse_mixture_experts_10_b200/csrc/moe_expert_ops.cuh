@@ -228,16 +228,32 @@ int launch_q4(int format, const q4::MatvecParams &p, const DeviceInfo &dev, cuda
     const int64_t live = std::min<int64_t>(p.N, p.pairs);
     q4::MatvecParams q = p;
     q.tiles = (int)cdiv(p.n, 16);
-    // split k over warps while one round of blocks (16 warps per SM) has room: with few tiles more rows stream at once
-    q.ks = 1;
-    while (q.ks < q4::kWarps && live * q.tiles * q.ks * 2 <= (int64_t)dev.sms * 16 && q.ks * 2 * q4::kChunk <= p.k)
-        q.ks *= 2;
-    const dim3 grid((unsigned)cdiv(q.tiles, q4::kWarps / q.ks), (unsigned)live);
+    // warps that share a tile: the fewest rounds of boxes for a block's share of the tiles (a round more for
+    // each tile's start and end); with few tiles a split of k keeps all warps streaming
+    const int64_t chunks = cdiv(p.k, q4::kChunk), mine = cdiv(live * q.tiles, dev.sms);
+    int64_t best = INT64_MAX;
+    for (int ks = 1; ks <= q4::kWarps && ks <= chunks; ks *= 2) {
+        const int64_t rounds = cdiv(mine, q4::kWarps / ks) * (cdiv(chunks, ks) + 1);
+        if (rounds < best) {
+            best = rounds;
+            q.ks = ks;
+        }
+    }
+    // pairs staged at a time and the ring's length: what shared memory holds
+    q.x_stride = q4::x_stride(p.k);
+    const size_t room = 227 * 1024 - 20 * 1024;   // 20 KB of static shared memory
+    q.slots = 4;
+    q.cols_pass = (int)std::min<int64_t>(p.pairs, q4::kMaxCols);
+    if (q4::matvec_smem(4, q.cols_pass, p.k, p.pairs) > room) q.slots = 3;
+    while (q.cols_pass > 1 && q4::matvec_smem(q.slots, q.cols_pass, p.k, p.pairs) > room) --q.cols_pass;
+    const size_t smem = q4::matvec_smem(q.slots, q.cols_pass, p.k, p.pairs);
+    if (smem > room) return MOE_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)std::min<int64_t>(dev.sms, live * q.tiles));
     auto *k = format == MOE_Q4_E2M1      ? q4::matvec_kernel<q4::E2M1, 5>
               : p.group_shift == 5       ? q4::matvec_kernel<q4::INT4, 5>
               : p.group_shift == 6       ? q4::matvec_kernel<q4::INT4, 6>
                                          : q4::matvec_kernel<q4::INT4, 7>;
-    return launch_pdl(k, grid, dim3(q4::kWarps * 32), q4::matvec_smem(p.pairs), s, map, q);
+    return launch_pdl(k, grid, dim3(q4::kWarps * 32), smem, s, map, q);
 }
 
 // Attributes of this file's kernels, set once per device with the others'.
