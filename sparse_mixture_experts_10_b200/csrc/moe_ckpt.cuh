@@ -27,6 +27,12 @@ enum { INT8 = 0, E4M3 = 1 };
 enum { GELU = 0, SWIGLU = 1, NONE = 2 };
 
 constexpr int kThreads = 256;
+constexpr int kUnroll = 4;   // 16-byte pieces of each operand that a lane loads before it computes
+
+__device__ __forceinline__ void load16(const void *p, uint32_t (&w)[4]) {
+    const uint4 u = __ldcs(static_cast<const uint4 *>(p));   // read once: ahead of everything else out of L2
+    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+}
 
 // 16 bytes of a row: 8 bf16 or 4 fp32 values.
 template <typename T>
@@ -34,9 +40,7 @@ struct Vec;
 template <>
 struct Vec<__nv_bfloat16> {
     static constexpr int N = 8;
-    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float (&v)[8]) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    static __device__ __forceinline__ void widen(const uint32_t (&w)[4], float (&v)[8]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[2 * i] = __uint_as_float(w[i] << 16);
@@ -59,9 +63,9 @@ struct Vec<__nv_bfloat16> {
 template <>
 struct Vec<float> {
     static constexpr int N = 4;
-    static __device__ __forceinline__ void load(const float *p, float (&v)[4]) {
-        const float4 u = *reinterpret_cast<const float4 *>(p);
-        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+    static __device__ __forceinline__ void widen(const uint32_t (&w)[4], float (&v)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
     }
     static __device__ __forceinline__ void store(float *p, const float (&v)[4]) {
         *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
@@ -92,24 +96,29 @@ __device__ __forceinline__ int scale_byte(float amax) {
     return min(max(e, -126), kMostExp<FMT>) + 127;
 }
 
-// Four values (already multiplied by 2^-e) as four bytes.
+// Four values v 2^-e (inv = 2^-e) as four bytes.  int8: 1.5 2^23 + x holds round(x), ties to even, in its low
+// bits (the product with a power of two is exact, so the fused sum rounds once); the conversion instructions
+// run at an eighth of its rate.
 template <int FMT>
-__device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d) {
+__device__ __forceinline__ uint32_t quant4(const float *v, float inv) {
     if (FMT == INT8) {
-        const uint32_t x = (uint32_t)__float2int_rn(a) & 0xffu, y = (uint32_t)__float2int_rn(b) & 0xffu;
-        const uint32_t z = (uint32_t)__float2int_rn(c) & 0xffu, w = (uint32_t)__float2int_rn(d) & 0xffu;
-        return x | (y << 8) | (z << 16) | (w << 24);
+        uint32_t b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(fmaf(v[i], inv, 12582912.0f));
+        return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
     }
-    const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * inv, v[1] * inv), __NV_SATFINITE, __NV_E4M3);
+    const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * inv, v[3] * inv), __NV_SATFINITE, __NV_E4M3);
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
+// int8: a byte q + 128 in the low bits of 2^23 is the float 2^23 + 128 + q.
 template <int FMT>
 __device__ __forceinline__ void dequant4(uint32_t q, float s, float *v) {
     if (FMT == INT8) {
+        const uint32_t u = q ^ 0x80808080u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = (float)((int)(q << (24 - 8 * i)) >> 24) * s;
+        for (int i = 0; i < 4; ++i) v[i] = (__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + i)) - 8388736.0f) * s;
     } else {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -123,23 +132,54 @@ __device__ __forceinline__ void dequant4(uint32_t q, float s, float *v) {
 
 // The scale of a byte; 255 stands for NaN.
 __device__ __forceinline__ float scale_value(uint32_t byte) {
-    return byte == 255u ? __int_as_float(0x7fffffff) : pow2i(max((int)byte, 1) - 127);
+    return byte == 255u ? __int_as_float(0x7fffffff) : pow2i((int)max(byte, 1u) - 127);
 }
 
-// NaN-keeping maximum of magnitudes, as unsigned bit patterns (NaN is above infinity).
-template <int N>
-__device__ __forceinline__ float amax_bits(const float (&v)[N], int lanes) {
+// NaN-keeping maximum of magnitudes over the lanes of a group, as bit patterns (NaN is above infinity).  Magnitudes
+// of bf16 compare as 16-bit integers, two at a time.
+template <typename T>
+__device__ __forceinline__ float amax_group(const uint32_t (&raw)[4], int lanes) {
     uint32_t m = 0;
+    if (sizeof(T) == 2) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+        for (int i = 0; i < 4; ++i) m = __vmaxu2(m, raw[i] & 0x7fff7fffu);
+        for (int o = lanes >> 1; o >= 1; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+        return __uint_as_float(max(m & 0xffff0000u, m << 16));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, raw[i] & 0x7fffffffu);
     for (int o = lanes >> 1; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     return __uint_as_float(m);
 }
 
-// Phi(v), the normal distribution function, and act / act' in the accuracy of the row type: exact-erf
-// GELU, sigmoid with expf and a division.
-__device__ __forceinline__ float phi(float v) { return 0.5f * (1.0f + erff(v * 0.70710678118654752f)); }
-__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
+// Phi(v), the normal distribution function, with its density, and the sigmoid, in the accuracy of the row type:
+// fp32 rows take erff, expf and a division.  bf16 rows (rounded to 2^-8 afterwards) take the special-function
+// unit: Phi(-|v|) = t (b1 + t (b2 + ...)) exp(-v^2 / 2), t = 1 / (1 + p |v| / sqrt 2), Abramowitz & Stegun,
+// Handbook of Mathematical Functions, formula 7.1.26 (absolute error of Phi at most 0.75e-7), whose
+// exponential is the density's too.
+template <typename T>
+__device__ __forceinline__ float phi(float v, float *density) {
+    constexpr float kDensity0 = 0.39894228040143268f;   // 1 / sqrt(2 pi)
+    if (sizeof(T) == 4) {
+        if (density) *density = expf(-0.5f * v * v) * kDensity0;
+        return 0.5f * (1.0f + erff(v * 0.70710678118654752f));
+    }
+    const float a = fabsf(v);
+    const float t = rcp_approx(fmaf(a, 0.2316418882663604f, 1.0f));   // p / sqrt 2, p = 0.3275911
+    const float e = ex2_approx(v * v * -0.7213475204444817f);         // log2(e) / 2
+    float q = fmaf(t, 0.5307027145f, -0.7265760135f);                 // a_i / 2
+    q = fmaf(t, q, 0.7107068705f);
+    q = fmaf(t, q, -0.142248368f);
+    q = fmaf(t, q, 0.127414796f);
+    const float below = q * t * e;
+    if (density) *density = e * kDensity0;
+    return v < 0.f ? below : 1.0f - below;
+}
+template <typename T>
+__device__ __forceinline__ float sigmoid(float v) {
+    if (sizeof(T) == 4) return 1.0f / (1.0f + expf(-v));
+    return rcp_approx(1.0f + ex2_approx(v * -1.4426950408889634f));
+}
 
 struct Params {
     const void *u;
@@ -156,45 +196,47 @@ struct Params {
     int row_warps;           // warps that share a row (a power of two, at most kThreads / 32)
 };
 
-// One vector of a row's half: the checkpoint's bytes written, the values left as they are.
+// One vector of a row's half: the checkpoint's bytes written.
 template <typename T, int FMT>
 __device__ __forceinline__ void save_vec(const Params &p, int64_t row, int half, int halves, int c, bool in,
-                                         const float (&v)[Vec<T>::N]) {
+                                         const uint32_t (&raw)[4], float (&v)[Vec<T>::N]) {
     constexpr int N = Vec<T>::N;
     const int lanes = (1 << p.group_shift) / N;
-    const int sb = scale_byte<FMT>(amax_bits(v, lanes));
+    const int sb = scale_byte<FMT>(amax_group<T>(raw, lanes));
+    Vec<T>::widen(raw, v);
     if (!in) return;
     const float inv = pow2i(sb == 255 ? 0 : 127 - sb);
-    float t[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) t[i] = sb == 255 ? 0.f : v[i] * inv;
-    if (FMT == INT8 && sb == kMostExp<FMT> + 127) {   // the cvt to e4m3 saturates by itself
-#pragma unroll
-        for (int i = 0; i < N; ++i) t[i] = fminf(fmaxf(t[i], -127.f), 127.f);
-    }
     uint32_t q[N / 4];
+    if (FMT == INT8 && sb == kMostExp<FMT> + 127) {   // may saturate (the conversion to e4m3 does so by itself)
+        float w[N];
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) q[i] = quant4<FMT>(t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3]);
+        for (int i = 0; i < N; ++i) w[i] = fminf(fmaxf(v[i] * inv, -127.f), 127.f);
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) q[i] = quant4<FMT>(w + 4 * i, 1.0f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) q[i] = sb == 255 ? 0u : quant4<FMT>(v + 4 * i, inv);
+    }
     Vec<T>::store_q(p.q + (row * halves + half) * p.width + c, q);
     if ((c & ((1 << p.group_shift) - 1)) == 0)
         p.s[(row * halves + half) * p.sgroups + (c >> p.group_shift)] = (uint8_t)sb;
 }
 
-template <typename T, int FMT>
-__device__ __forceinline__ void load_vec(const Params &p, int64_t row, int half, int halves, int c, bool in,
-                                         float (&v)[Vec<T>::N]) {
-    constexpr int N = Vec<T>::N;
-    uint32_t q[N / 4];
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) q[i] = 0;
-    if (in) {
+// One vector of a checkpoint: fetched as bytes, widened later.
+template <typename T>
+struct Saved {
+    uint32_t q[Vec<T>::N / 4], s;
+    __device__ __forceinline__ void fetch(const Params &p, int64_t row, int half, int halves, int c) {
         Vec<T>::load_q(p.q_in + (row * halves + half) * p.width + c, q);
-        s = scale_value(p.s_in[(row * halves + half) * p.sgroups + (c >> p.group_shift)]);
+        s = p.s_in[(row * halves + half) * p.sgroups + (c >> p.group_shift)];
     }
+    template <int FMT>
+    __device__ __forceinline__ void widen(float (&v)[Vec<T>::N]) const {
+        const float scale = scale_value(s);
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) dequant4<FMT>(q[i], s, v + 4 * i);
-}
+        for (int i = 0; i < Vec<T>::N / 4; ++i) dequant4<FMT>(q[i], scale, v + 4 * i);
+    }
+};
 
 template <typename T, int ACT, int FMT>
 __global__ void __launch_bounds__(kThreads) forward_kernel(const Params p) {
@@ -204,20 +246,31 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const Params p) {
     const int64_t row = (int64_t)blockIdx.x * ((kThreads / 32) / p.row_warps) + warp / p.row_warps;
     if (row >= p.rows) return;
     const T *u = static_cast<const T *>(p.u) + row * p.ldu;
-    for (int c0 = (warp % p.row_warps) * 32 * N; c0 < p.width; c0 += p.row_warps * 32 * N) {
-        const int c = c0 + lane * N;
-        const bool in = c < p.width;
-        float a[N] = {}, b[N] = {}, o[N];
-        if (in) {
-            Vec<T>::load(u + c, a);
-            if (ACT == SWIGLU) Vec<T>::load(u + p.width + c, b);
-        }
-        save_vec<T, FMT>(p, row, 0, kHalves, c, in, a);
-        if (ACT == SWIGLU) save_vec<T, FMT>(p, row, 1, kHalves, c, in, b);
-        if (ACT == NONE) continue;
+    const int stride = p.row_warps * 32 * N;
+    for (int c0 = (warp % p.row_warps) * 32 * N; c0 < p.width; c0 += kUnroll * stride) {
+        uint32_t ra[kUnroll][4] = {}, rb[kUnroll][4] = {};
 #pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = ACT == GELU ? a[i] * phi(a[i]) : a[i] * sigmoid(a[i]) * b[i];
-        if (in) Vec<T>::store(static_cast<T *>(p.h) + row * p.ldh + c, o);
+        for (int k = 0; k < kUnroll; ++k) {
+            const int c = c0 + k * stride + lane * N;
+            if (c < p.width) {
+                load16(u + c, ra[k]);
+                if (ACT == SWIGLU) load16(u + p.width + c, rb[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+            if (c0 + k * stride >= p.width) break;   // warp-uniform
+            const int c = c0 + k * stride + lane * N;
+            const bool in = c < p.width;
+            float a[N], b[N], o[N];
+            save_vec<T, FMT>(p, row, 0, kHalves, c, in, ra[k], a);
+            if (ACT == SWIGLU) save_vec<T, FMT>(p, row, 1, kHalves, c, in, rb[k], b);
+            if (ACT == NONE || !in) continue;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                o[i] = ACT == GELU ? a[i] * phi<T>(a[i], nullptr) : a[i] * sigmoid<T>(a[i]) * b[i];
+            Vec<T>::store(static_cast<T *>(p.h) + row * p.ldh + c, o);
+        }
     }
 }
 
@@ -233,7 +286,9 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const Params p, int halv
             const int c = c0 + lane * N;
             if (c >= p.width) continue;
             float v[N];
-            load_vec<T, FMT>(p, row, half, halves, c, true, v);
+            Saved<T> x;
+            x.fetch(p, row, half, halves, c);
+            x.template widen<FMT>(v);
             Vec<T>::store(static_cast<T *>(p.h) + row * p.ldh + (int64_t)half * p.width + c, v);
         }
 }
@@ -252,33 +307,48 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const Params p) {
         const float w = p.w ? p.w[row] : 1.0f;
         const T *dh = static_cast<const T *>(p.dh) + row * p.ldh;
         T *du = static_cast<T *>(p.du) + row * p.ldu;
-        for (int c0 = (warp % p.row_warps) * 32 * N; c0 < p.width; c0 += p.row_warps * 32 * N) {
-            const int c = c0 + lane * N;
-            const bool in = c < p.width;
-            float a[N], b[N] = {}, d[N] = {}, hv[N], da[N], db[N];
-            if (in) Vec<T>::load(dh + c, d);
-            load_vec<T, FMT>(p, row, 0, kHalves, c, in, a);
-            if (ACT == SWIGLU) load_vec<T, FMT>(p, row, 1, kHalves, c, in, b);
+        const int stride = p.row_warps * 32 * N;
+        for (int c0 = (warp % p.row_warps) * 32 * N; c0 < p.width; c0 += kUnroll * stride) {
+            uint32_t rd[kUnroll][4] = {};
+            Saved<T> xa[kUnroll], xb[kUnroll];
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float g = w * d[i];
-                if (ACT == GELU) {
-                    const float ph = phi(a[i]);
-                    hv[i] = a[i] * ph;
-                    da[i] = g * (ph + a[i] * expf(-0.5f * a[i] * a[i]) * 0.39894228040143268f);
-                } else {
-                    const float sg = sigmoid(a[i]), si = a[i] * sg;
-                    hv[i] = si * b[i];
-                    da[i] = g * b[i] * sg * (1.0f + a[i] * (1.0f - sg));
-                    db[i] = g * si;
+            for (int k = 0; k < kUnroll; ++k) {
+                const int c = c0 + k * stride + lane * N;
+                if (c < p.width) {
+                    load16(dh + c, rd[k]);
+                    xa[k].fetch(p, row, 0, kHalves, c);
+                    if (ACT == SWIGLU) xb[k].fetch(p, row, 1, kHalves, c);
                 }
-                if (in) dot = fmaf(d[i], hv[i], dot);
-                hv[i] *= w;
             }
-            if (!in) continue;
-            Vec<T>::store(du + c, da);
-            if (ACT == SWIGLU) Vec<T>::store(du + p.width + c, db);
-            if (p.hw) Vec<T>::store(static_cast<T *>(p.hw) + row * p.ldh + c, hv);
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) {
+                const int c = c0 + k * stride + lane * N;
+                if (c >= p.width) break;
+                float a[N], b[N], d[N], hv[N], da[N], db[N];
+                Vec<T>::widen(rd[k], d);
+                xa[k].template widen<FMT>(a);
+                if (ACT == SWIGLU) xb[k].template widen<FMT>(b);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float g = w * d[i];
+                    if (ACT == GELU) {
+                        float density;
+                        const float ph = phi<T>(a[i], &density);
+                        hv[i] = a[i] * ph;
+                        da[i] = g * fmaf(a[i], density, ph);
+                    } else {
+                        const float sg = sigmoid<T>(a[i]), si = a[i] * sg;
+                        hv[i] = si * b[i];
+                        da[i] = g * b[i] * sg * (1.0f + a[i] * (1.0f - sg));
+                        db[i] = g * si;
+                    }
+                    dot = fmaf(d[i], hv[i], dot);
+                    hv[i] *= w;
+                }
+                Vec<T>::store(du + c, da);
+                if (ACT == SWIGLU) Vec<T>::store(du + p.width + c, db);
+                if (p.hw) Vec<T>::store(static_cast<T *>(p.hw) + row * p.ldh + c, hv);
+            }
         }
     }
     if (!p.dw) return;

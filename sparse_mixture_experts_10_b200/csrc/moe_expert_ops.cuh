@@ -166,10 +166,10 @@ int make_ckpt_params(const moe_ckpt *d, int64_t rows, ckpt::Params *p) {
     p->width = d->width;
     p->group_shift = d->group == 32 ? 5 : d->group == 64 ? 6 : 7;
     p->sgroups = (int)cdiv(d->width, d->group);
-    // warps of a block that share a row: as many as the row has 512-byte pieces, at most all of them
-    const int64_t pieces = cdiv((int64_t)d->width * es, 512);
+    // warps of a block that share a row: as many as the row has pieces for (512 bytes a load, kUnroll loads at a time)
+    const int64_t pieces = cdiv((int64_t)d->width * es, 512 * ckpt::kUnroll);
     p->row_warps = 1;
-    while (p->row_warps < ckpt::kThreads / 32 && p->row_warps < pieces) p->row_warps *= 2;
+    while (p->row_warps < ckpt::kThreads / 32 && p->row_warps * 2 <= pieces) p->row_warps *= 2;
     return MOE_OK;
 }
 
