@@ -55,7 +55,7 @@ int make_gmm_plan(const moe_gmm *d, int64_t rows, GmmPlan *out) {
     return MOE_OK;
 }
 
-template <typename T, typename TO, int KIND>
+template <int KIND>
 int launch_gmm_simt(gmm::Params p, const DeviceInfo &dev, cudaStream_t s) {
     const int64_t cols = KIND == gmm::NT ? p.n : p.k;
     p.n_tiles = (int)cdiv(cols, gmm::kTile);
@@ -69,7 +69,7 @@ int launch_gmm_simt(gmm::Params p, const DeviceInfo &dev, cudaStream_t s) {
     if (upper > INT32_MAX) return MOE_ERR_UNSUPPORTED;
     p.total = (int)upper;
     const unsigned grid = (unsigned)std::min<int64_t>(upper, (int64_t)dev.sms * 6);
-    return launch_pdl(gmm::simt_kernel<T, TO, KIND>, dim3(grid), dim3(256), 0, s, p);
+    return launch_pdl(gmm::simt_kernel<KIND>, dim3(grid), dim3(gmm::kSimtThreads), 0, s, p);
 }
 
 // bf16 tensor of up to four dimensions (d[0] contiguous, the others with strides of st elements), 128-byte swizzle.
@@ -145,7 +145,7 @@ int launch_gmm_tc(gmm::Params p, const DeviceInfo &dev, cudaStream_t s) {
 
 template <int KIND>
 int launch_gmm(const moe_gmm *d, const gmm::Params &p, const DeviceInfo &dev, cudaStream_t s) {
-    if (d->dtype == MOE_F32) return launch_gmm_simt<float, float, KIND>(p, dev, s);
+    if (d->dtype == MOE_F32) return launch_gmm_simt<KIND>(p, dev, s);
     if (d->out_dtype == MOE_F32) return launch_gmm_tc<KIND, float>(p, dev, s);
     return launch_gmm_tc<KIND, __nv_bfloat16>(p, dev, s);
 }

@@ -83,47 +83,32 @@ struct Params {
     uint64_t timeout_ns;
 };
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T *p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xffff0000u));
-}
-__device__ __forceinline__ float4 get4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ float4 get4(const __nv_bfloat16 *p) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xffff0000u));
-}
-__device__ __forceinline__ void put4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
-__device__ __forceinline__ void put4(__nv_bfloat16 *p, float4 v) {
-    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-}
+// CUDA-core kernel for fp32 operands: 64 x 64 tiles, slices of 32 along the
+// contraction in two shared-memory buffers (the next slice travels in registers
+// meanwhile), two halves of 128 threads with 8 x 4 results each as pairs of rows
+// (one f32x2 multiply-add for two); either half takes 16 of a slice's 32 steps,
+// and their fp32 sums are added at the end.  12 floats are read from shared
+// memory for 32 multiply-adds; the second half doubles the warps that hide
+// the latencies where there are few tiles.
+constexpr int kTile = 64, kSlice = 32, kSimtThreads = 256;
 
-// CUDA-core kernel: 64 x 64 tiles, slices of 16 along the contraction, 256
-// threads with 4 x 4 results each, sums in fp32 in ascending order.
-constexpr int kTile = 64, kSlice = 16;
-
-template <typename T, typename TO, int KIND>
-__global__ void __launch_bounds__(256) simt_kernel(const Params p) {
+template <int KIND>
+__global__ void __launch_bounds__(kSimtThreads) simt_kernel(const Params p) {
     pdl_enter();
-    __shared__ __align__(16) float As[kSlice][kTile + 4];
-    __shared__ __align__(16) float Bs[kSlice][kTile + 4];
+    __shared__ __align__(16) float s_ab[2][2][kSlice][kTile + 4];   // [operand][buffer]
+    auto &As = s_ab[0], &Bs = s_ab[1];
     __shared__ int s_off[kMaxGroups + 1], s_cum[kMaxGroups + 1];
     const int tid = threadIdx.x;
     if (tid < 32) load_segments(p.row_offsets, p.G, p.rows, kTile, s_off, s_cum);
     __syncthreads();
-    const T *A = static_cast<const T *>(p.A), *B = static_cast<const T *>(p.B);
+    const float *A = static_cast<const float *>(p.A), *B = static_cast<const float *>(p.B);
     const int cols = KIND == NT ? p.n : p.k;   // columns of the result
     const int total = KIND == TN ? p.total : s_cum[p.G] * p.n_tiles;
-    const int tx = tid & 15, ty = tid >> 4;
-    // a K-major operand (rows of the tile contiguous along the contraction): thread -> row tid/4, 4 values from
-    // (tid%4)*4; an MN-major one: thread -> contraction index tid/16, 4 values from (tid%16)*4
-    const int kr = tid >> 2, kc = (tid & 3) * 4, mr = tid >> 4, mc = (tid & 15) * 4;
+    const int half = tid >> 7, tx = tid & 15, ty = (tid & 127) >> 4;
+    // a K-major operand (rows of the tile contiguous along the contraction): thread -> row tid/4, 8 values from
+    // (tid%4)*8; an MN-major one: thread -> contraction index tid/8, 8 values from (tid%8)*8
+    constexpr int kV = 2;   // 16-byte loads of each operand
+    const int kr = tid >> 2, kc = (tid & 3) * 8, mr = tid >> 3, mc = (tid & 7) * 8;
     for (int i = blockIdx.x; i < total; i += gridDim.x) {
         int g, m0, n0, m_hi, lo = 0, hi;   // rows (or A columns) m0..m_hi, result columns from n0, contraction lo..hi
         if (KIND == TN) {
@@ -143,55 +128,100 @@ __global__ void __launch_bounds__(256) simt_kernel(const Params p) {
             m_hi = s_off[g + 1];
             hi = KIND == NT ? p.k : p.n;
         }
-        const T *Bg = KIND == TN ? B : B + (int64_t)g * p.n * p.ldb;
-        float4 a, b;
+        const float *Bg = KIND == TN ? B : B + (int64_t)g * p.n * p.ldb;
+        float4 a[kV], b[kV];
         auto fetch = [&](int kk) {
-            const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (KIND == TN) a = kk + mr < hi && m0 + mc < m_hi ? load4(A + (kk + mr) * p.lda + m0 + mc) : z;
-            else a = m0 + kr < m_hi && kk + kc < hi ? load4(A + (m0 + kr) * p.lda + kk + kc) : z;
-            if (KIND == NT) b = n0 + kr < cols && kk + kc < hi ? load4(Bg + (int64_t)(n0 + kr) * p.ldb + kk + kc) : z;
-            else b = kk + mr < hi && n0 + mc < cols ? load4(Bg + (int64_t)(kk + mr) * p.ldb + n0 + mc) : z;
-        };
-        float acc[4][4] = {};
-        if (lo < hi) fetch(lo);
-        for (int kk = lo; kk < hi; kk += kSlice) {
-            if (KIND == TN) {
-                *reinterpret_cast<float4 *>(&As[mr][mc]) = a;
-            } else {
-                As[kc][kr] = a.x; As[kc + 1][kr] = a.y; As[kc + 2][kr] = a.z; As[kc + 3][kr] = a.w;
-            }
-            if (KIND == NT) {
-                Bs[kc][kr] = b.x; Bs[kc + 1][kr] = b.y; Bs[kc + 2][kr] = b.z; Bs[kc + 3][kr] = b.w;
-            } else {
-                *reinterpret_cast<float4 *>(&Bs[mr][mc]) = b;
-            }
-            __syncthreads();
-            if (kk + kSlice < hi) fetch(kk + kSlice);
 #pragma unroll
-            for (int q = 0; q < kSlice; ++q) {
-                const float4 av = *reinterpret_cast<const float4 *>(&As[q][ty * 4]);
-                const float4 bv = *reinterpret_cast<const float4 *>(&Bs[q][tx * 4]);
-                const float ar[4] = {av.x, av.y, av.z, av.w}, br[4] = {bv.x, bv.y, bv.z, bv.w};
+            for (int h = 0; h < kV; ++h) {
+                const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+                const int kh = kc + 4 * h, mh = mc + 4 * h;
+                auto at = [](const float *q) { return __ldg(reinterpret_cast<const float4 *>(q)); };
+                if (KIND == TN) a[h] = kk + mr < hi && m0 + mh < m_hi ? at(A + (kk + mr) * p.lda + m0 + mh) : z;
+                else a[h] = m0 + kr < m_hi && kk + kh < hi ? at(A + (m0 + kr) * p.lda + kk + kh) : z;
+                if (KIND == NT) b[h] = n0 + kr < cols && kk + kh < hi ? at(Bg + (n0 + kr) * p.ldb + kk + kh) : z;
+                else b[h] = kk + mr < hi && n0 + mh < cols ? at(Bg + (kk + mr) * p.ldb + n0 + mh) : z;
+            }
+        };
+        auto put = [&](int buf) {
+#pragma unroll
+            for (int h = 0; h < kV; ++h) {
+                const int kh = kc + 4 * h, mh = mc + 4 * h;
+                if (KIND == TN) {
+                    *reinterpret_cast<float4 *>(&As[buf][mr][mh]) = a[h];
+                } else {
+                    As[buf][kh][kr] = a[h].x; As[buf][kh + 1][kr] = a[h].y;
+                    As[buf][kh + 2][kr] = a[h].z; As[buf][kh + 3][kr] = a[h].w;
+                }
+                if (KIND == NT) {
+                    Bs[buf][kh][kr] = b[h].x; Bs[buf][kh + 1][kr] = b[h].y;
+                    Bs[buf][kh + 2][kr] = b[h].z; Bs[buf][kh + 3][kr] = b[h].w;
+                } else {
+                    *reinterpret_cast<float4 *>(&Bs[buf][mr][mh]) = b[h];
+                }
+            }
+        };
+        uint64_t acc[4][4];   // [pair of rows][column]
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) acc[x][y] = 0;
+        int buf = 0;
+        if (lo < hi) {
+            fetch(lo);
+            put(0);
+        }
+        __syncthreads();
+        for (int kk = lo; kk < hi; kk += kSlice, buf ^= 1) {
+            const bool more = kk + kSlice < hi;
+            if (more) fetch(kk + kSlice);
+#pragma unroll
+            for (int q0 = 0; q0 < kSlice / 2; ++q0) {
+                const int q = half * (kSlice / 2) + q0;
+                const ulonglong2 a0 = *reinterpret_cast<const ulonglong2 *>(&As[buf][q][ty * 8]);
+                const ulonglong2 a1 = *reinterpret_cast<const ulonglong2 *>(&As[buf][q][ty * 8 + 4]);
+                const float4 bv = *reinterpret_cast<const float4 *>(&Bs[buf][q][tx * 4]);
+                const uint64_t ar[4] = {a0.x, a0.y, a1.x, a1.y};
+                const uint64_t br[4] = {f2_splat(bv.x), f2_splat(bv.y), f2_splat(bv.z), f2_splat(bv.w)};
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) acc[x][y] = fmaf(ar[x], br[y], acc[x][y]);
+                    for (int y = 0; y < 4; ++y) acc[x][y] = f2_fma(ar[x], br[y], acc[x][y]);
             }
+            if (more) put(buf ^ 1);
             __syncthreads();
         }
+        // the second half's sums, through the operands' buffers
+        uint64_t *s_sum = reinterpret_cast<uint64_t *>(&s_ab[0][0][0][0]) + (tid & 127);
+        if (half) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) s_sum[x * 128] = acc[x >> 2][x & 3];
+        }
+        __syncthreads();
+        if (!half) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) acc[x >> 2][x & 3] = f2_add(acc[x >> 2][x & 3], s_sum[x * 128]);
+        }
+        __syncthreads();
         const int c = n0 + tx * 4;
-        if (c >= cols) continue;
+        if (half || c >= cols) continue;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            const int r = m0 + ty * 4 + x;
-            if (r >= m_hi) continue;
-            TO *dst = static_cast<TO *>(p.C) + ((KIND == TN ? (int64_t)g * p.n : 0) + r) * p.ldc + c;
-            float4 v = make_float4(acc[x][0], acc[x][1], acc[x][2], acc[x][3]);
-            if (KIND == TN && p.accumulate) {
-                const float4 o = get4(dst);
-                v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+            float v[2][4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) f2_unpack(acc[x][y], v[0][y], v[1][y]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = m0 + ty * 8 + 2 * x + h;
+                if (r >= m_hi) continue;
+                float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.C) +
+                                                         ((KIND == TN ? (int64_t)g * p.n : 0) + r) * p.ldc + c);
+                float4 o = make_float4(v[h][0], v[h][1], v[h][2], v[h][3]);
+                if (KIND == TN && p.accumulate) {
+                    const float4 was = *dst;
+                    o = make_float4(was.x + o.x, was.y + o.y, was.z + o.z, was.w + o.w);
+                }
+                *dst = o;
             }
-            put4(dst, v);
         }
     }
 }
