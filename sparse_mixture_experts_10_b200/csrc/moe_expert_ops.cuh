@@ -210,21 +210,23 @@ int make_q4_params(const moe_q4 *d, q4::Params *p) {
     return MOE_OK;
 }
 
-// Codes [rows, k / 2] as boxes of 8 rows x 128 bytes, 128-byte swizzle.
-int make_map_codes(CUtensorMap *m, const uint8_t *codes, int64_t rows, int64_t row_bytes) {
+// Codes [N, n, k / 2] as boxes of box_tiles tiles x 128 bytes, 128-byte swizzle: 16 rows a tile, or (halves) 8 rows of
+// either half of the n rows.
+int make_map_codes(CUtensorMap *m, const uint8_t *codes, int64_t N, int64_t n, int64_t row_bytes, bool halves,
+                   int box_tiles) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return MOE_ERR_CUDA;
-    const cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)row_bytes};
-    const cuuint32_t box[2] = {128u, 8u}, estr[2] = {1u, 1u};
-    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(codes), dims, strides, box, estr,
+    const cuuint64_t rows = (cuuint64_t)(halves ? n / 2 : n), rb = (cuuint64_t)row_bytes;
+    const cuuint64_t dims[4] = {rb, rows, halves ? 2u : 1u, (cuuint64_t)N}, strides[3] = {rb, rows * rb, (cuuint64_t)n * rb};
+    const cuuint32_t box[4] = {128u, (cuuint32_t)(box_tiles * (halves ? 8 : 16)), halves ? 2u : 1u, 1u};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t *>(codes), dims, strides, box, estr,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
 }
 
 int launch_q4(int format, const q4::MatvecParams &p, const DeviceInfo &dev, cudaStream_t s) {
-    CUtensorMap map;
-    MOE_TRY(make_map_codes(&map, p.codes, (int64_t)p.N * p.n, p.k / 2));
     const int64_t live = std::min<int64_t>(p.N, p.pairs);
     q4::MatvecParams q = p;
     q.tiles = (int)cdiv(p.n, 16);
@@ -241,19 +243,23 @@ int launch_q4(int format, const q4::MatvecParams &p, const DeviceInfo &dev, cuda
     }
     // pairs staged at a time and the ring's length: what shared memory holds
     q.x_stride = q4::x_stride(p.k);
-    const size_t room = 227 * 1024 - 20 * 1024;   // 20 KB of static shared memory
+    const size_t room = 227 * 1024 - 32 * 1024;   // 32 KB of static shared memory
     q.slots = 4;
     q.cols_pass = (int)std::min<int64_t>(p.pairs, q4::kMaxCols);
     if (q4::matvec_smem(4, q.cols_pass, p.k, p.pairs) > room) q.slots = 3;
     while (q.cols_pass > 1 && q4::matvec_smem(q.slots, q.cols_pass, p.k, p.pairs) > room) --q.cols_pass;
     const size_t smem = q4::matvec_smem(q.slots, q.cols_pass, p.k, p.pairs);
     if (smem > room) return MOE_ERR_UNSUPPORTED;
+    // a copy is four tiles where a block's step has as many: a step at an expert's end then reads little too much
+    q.box_tiles = std::min(4, q4::kWarps / q.ks);
+    CUtensorMap map;
+    MOE_TRY(make_map_codes(&map, q.codes, q.N, q.n, q.k / 2, q.act == MOE_ACT_SWIGLU, q.box_tiles));
     const dim3 grid((unsigned)std::min<int64_t>(dev.sms, live * q.tiles));
     auto *k = format == MOE_Q4_E2M1      ? q4::matvec_kernel<q4::E2M1, 5>
               : p.group_shift == 5       ? q4::matvec_kernel<q4::INT4, 5>
               : p.group_shift == 6       ? q4::matvec_kernel<q4::INT4, 6>
                                          : q4::matvec_kernel<q4::INT4, 7>;
-    return launch_pdl(k, grid, dim3(q4::kWarps * 32), smem, s, map, q);
+    return launch_pdl(k, grid, dim3(q4::kThreadsMv), smem, s, map, q);
 }
 
 // Attributes of this file's kernels, set once per device with the others'.

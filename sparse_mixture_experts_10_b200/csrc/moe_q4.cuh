@@ -9,6 +9,8 @@
 //   a[i] = sum_j W[e][i, j] x[j],  y[p] = gate[p] * act(a).
 #pragma once
 
+#include <type_traits>
+
 #include "moe_common.cuh"
 
 namespace moe {
@@ -55,30 +57,34 @@ __device__ __forceinline__ float gelu(float v) { return 0.5f * v * (1.0f + erff(
 __device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
 
 // ---------------------------------------------------------------- the products
-// One persistent block per SM takes an even share of the live experts' 16-row
-// tiles of W[e] (SwiGLU: 8 gate rows and the 8 up rows beside them, so that a
-// lane ends with both).  Its warps multiply tiles with up to 16 of the expert's
-// pairs as columns of m16n8k16 products (bf16 x bf16 -> fp32); where there are
-// few tiles, ks warps share a tile along k and their sums are added in order.
-// A code is at most 4 bits, exact in bf16; the products of a group are summed
-// in fp32 by the tensor core and enter the result with one fp32 multiply-add by
-// the group's scale, so nothing is rounded to fewer bits before the end.
+// One persistent block per SM takes an even share (by cost: tiles times lots of
+// pairs) of the live experts' 16-row tiles of W[e] (SwiGLU: 8 gate rows and the
+// 8 up rows beside them, so that a lane ends with both).  16 consumer warps
+// multiply a tile each with up to 16 of the expert's pairs as columns of
+// m16n8k16 products (bf16 x bf16 -> fp32); where there are few tiles, ks warps
+// share a tile along k and their sums are added in order.  A code is at most
+// 4 bits, exact in bf16; the products of a group are summed in fp32 by the
+// tensor core and enter the result with one fp32 multiply-add by the group's
+// scale, so nothing is rounded to fewer bits before the end.
 //
 // HBM (0.5 byte per weight) is the floor; what is in the way of it is the
-// instructions that unpack the codes (about 11 per 8 codes and lane).  Each warp
-// streams its own boxes of 16 rows x 128 bytes (256 values of k) through a
-// ring that runs on from tile to tile, without a block barrier.  The 128-byte
-// swizzle lets the fragment reads (4 bytes per lane: 8 rows x 16 bytes) hit 32
-// different banks.  Inside a group the order of k is free: lane t of a row takes
-// the 8 codes of one 32-bit word, as pairs (i, i + 4) that one mask each
-// extracts; the expert's rows of x are staged in shared memory in that order.
-constexpr int kWarps = 16, kMaxSlots = 4, kBoxBytes = 2048, kChunk = 256;
+// instructions that unpack the codes (about 11 per 8 codes and lane).  So one
+// more warp does all the copies: slices of 256 values of k of 16 tiles (32 KB)
+// go through a ring of 3 or 4 that runs on from tile to tile and from expert to
+// expert.  The 128-byte swizzle lets the fragment reads (4 bytes per lane: 8
+// rows x 16 bytes) hit 32 different banks.  Inside a group the order of k is
+// free: lane t of a row takes the 8 codes of one 32-bit word, as pairs (i, i + 4)
+// that one mask each extracts; the expert's rows of x are staged in shared
+// memory in that order.
+constexpr int kWarps = 16, kThreadsMv = (kWarps + 1) * 32;
+constexpr int kMaxSlots = 4, kSlotBytes = kWarps * 2048, kChunk = 256;
 constexpr int kMaxPairs = 4096, kMaxExperts = 1024, kMaxCols = 16;
 
 struct MatvecParams : Params {
     int act, y_f32;
     int tiles, ks;         // 16-row tiles of an expert; warps that share a tile (split k)
-    int slots;             // boxes of a warp's ring (3 or 4)
+    int box_tiles;         // tiles of one copy (a tensor-map box of 128 bytes x 16 rows each)
+    int slots;             // slices in the ring (3 or 4)
     int cols_pass;         // pairs staged at a time (at most kMaxCols)
     uint32_t x_stride;     // bytes between staged rows of x
     uint64_t timeout_ns;
@@ -142,160 +148,141 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A warp's walk over its boxes: tiles tile, tile + step, ... (below end), in each the chunks lo..hi-1.
-struct Walk {
-    int tile, chunk, left;   // left: boxes not reached yet, this one included
-    __device__ __forceinline__ void next(int lo, int hi, int step) {
-        --left;
-        if (++chunk == hi) {
-            chunk = lo;
-            tile += step;
-        }
-    }
-};
-
 __device__ __forceinline__ void group_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// One warp's tiles of expert e against the staged columns (NB blocks of 8; list[0..cnt) their pairs).
+__device__ __forceinline__ void tma_load_codes(const CUtensorMap *map, uint64_t *bar, void *dst, int c0, int c1, int e) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+        "[%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(0), "r"(e)
+        : "memory");
+}
+
+// Where a consumer warp is in the ring.
+struct Ring {
+    uint32_t base;      // shared-memory address of the slots
+    uint64_t *full, *empty;
+    int slot = 0;
+    uint32_t phase = 0;
+    bool ok = true;     // false: a wait ran out (status word); nothing more is computed
+};
+
+// Tiles tile0..tile1-1 of expert e against the staged columns (NB blocks of 8; list[0..cnt) their pairs).
 template <int FMT, int SHIFT, int NB>
-__device__ __forceinline__ bool run_tiles(const MatvecParams &p, const CUtensorMap *map, uint8_t *ring, uint64_t *bars,
-                                          uint32_t &phases, int &slot, const uint8_t *s_x, float (*part)[8][32], int e,
-                                          int tile0, int tile1, const uint16_t *list, int cnt, bool ok) {
+__device__ __forceinline__ void run_tiles(const MatvecParams &p, Ring &ring, uint32_t s_x, float (*part)[8][32], int e,
+                                          int tile0, int tile1, const uint16_t *list, int cnt) {
+    using Raw = typename std::conditional<FMT == INT4, unsigned short, unsigned char>::type;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const bool swiglu = p.act == SWIGLU;
     const int cols = swiglu ? p.n / 2 : p.n;
-    const int share = warp % p.ks, step = kWarps / p.ks;
-    const int chunks = (p.k + kChunk - 1) / kChunk;
-    const int lo = chunks * share / p.ks, hi = chunks * (share + 1) / p.ks;
-    const int first = tile0 + warp / p.ks, mine = first < tile1 ? (tile1 - first + step - 1) / step : 0;
-    const int64_t base = (int64_t)e * p.n;
-    const int half1 = swiglu ? cols : 8;   // distance of the tile's second 8 rows from its first
-    const int rows_tile = swiglu ? 8 : 16;
-    const int total = mine * (hi - lo);
-    Walk in{first, lo, total}, sc{first, lo, total};
-    // The scales of a tile's rows into L2, when its first box is issued: they are read one box ahead of their use, which
-    // covers the latency of L2 but not of HBM.
-    constexpr int kScaleBytes = FMT == INT4 ? 2 : 1;
-    auto prefetch_scales = [&](int tile) {
-        const int row = tile * rows_tile + (lane & 7) + (lane & 8 ? half1 : 0);
-        if (row >= p.n) return;
-        const char *s = static_cast<const char *>(p.scales) + (base + row) * p.groups * kScaleBytes;
-        const int b1 = min((hi * kChunk) >> SHIFT, p.groups) * kScaleBytes;
-        for (int b = ((lo * kChunk) >> SHIFT) * kScaleBytes + (lane >> 4) * 32; b < b1 + 31; b += 64)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(s + min(b, b1 - 1)));
-    };
-    auto issue = [&](int sl) {   // lane 0: the next box into slot sl
-        const int r = (int)base + in.tile * rows_tile;
-        mbar_arrive_expect_tx(&bars[sl], kBoxBytes);
-        tma_load_2d(map, &bars[sl], ring + sl * kBoxBytes, in.chunk * (kChunk / 2), r);
-        tma_load_2d(map, &bars[sl], ring + sl * kBoxBytes + 1024, in.chunk * (kChunk / 2), r + half1);
-    };
-    int sl = slot, flying = 0;   // boxes issued and not waited for
-    for (int i = 0; i < p.slots && in.left > 0 && ok; ++i) {
-        if (in.chunk == lo) prefetch_scales(in.tile);
-        if (lane == 0) issue(sl);
-        ++flying;
-        in.next(lo, hi, step);
-        if (++sl == p.slots) sl = 0;
-    }
-    // What a lane holds of a box: the scales of the rows g and g + 8 for the 32-value pieces 2t and 2t + 1 (one scale
-    // for both with groups of 64 and more; 0 past the last group).
-    constexpr int kN = SHIFT == 5 ? 2 : 1;
-    // They are loaded as they are and widened a box later, so that nothing waits for them in between.
-    int64_t sr0 = 0, sr1 = 0;   // the rows' first scales (the second row may be no row of this expert: the first again)
-    auto scale_rows = [&] {
-        const int64_t r = base + sc.tile * rows_tile + g;
-        sr0 = r * p.groups;
-        sr1 = sc.tile * rows_tile + half1 + g < p.n ? (r + half1) * p.groups : sr0;
-    };
-    if (mine > 0) scale_rows();
-    uint32_t next[2 * kN] = {}, next_in = 0;   // the next box's, and which of them are inside the row
-    float s0[2 * kN] = {};
-    auto load_scales = [&] {
-        next_in = 0;
-        if (sc.left <= 0) return;
-#pragma unroll
-        for (int j = 0; j < kN; ++j) {
-            const int at = (sc.chunk * kChunk + (2 * t + j) * 32) >> SHIFT, in = min(at, p.groups - 1);
-            next_in |= (at < p.groups ? 1u : 0u) << j;
-            next[j] = raw_scale<FMT>(p.scales, sr0 + in);
-            next[kN + j] = raw_scale<FMT>(p.scales, sr1 + in);
-        }
-        const int was = sc.tile;
-        sc.next(lo, hi, step);
-        if (sc.tile != was && sc.left > 0) scale_rows();
-    };
-    auto take_scales = [&] {
-#pragma unroll
-        for (int j = 0; j < 2 * kN; ++j) s0[j] = (next_in >> (j % kN)) & 1u ? wide_scale<FMT>(next[j]) : 0.f;
-    };
-    load_scales();
-    take_scales();
-    __syncthreads();   // x is staged
-    constexpr int kPieces = 1 << (SHIFT - 5);   // per scale: their products are added up before it is applied
-    // the word of piece c in the swizzled box: 16-byte unit c ^ g of row g; bits 4-6 of the rest are 0
-    const uint32_t at = (uint32_t)(g * 128 + t * 4 + (g << 4));
+    const int share = warp % p.ks, step = kWarps / p.ks, mine = warp / p.ks;
+    const int chunks = (p.k + kChunk - 1) / kChunk, rounds = (chunks + p.ks - 1) / p.ks;
+    const int rows_tile = swiglu ? 8 : 16, half1 = swiglu ? cols : 8;   // distance of a tile's second 8 rows
+    const Raw *scales = static_cast<const Raw *>(p.scales) + (int64_t)e * p.n * p.groups;
+    // the slot holds copies of box_tiles tiles; SwiGLU: their gate rows, then their up rows
+    const int in_box = mine % p.box_tiles;
+    const uint32_t box = (uint32_t)((share * (step / p.box_tiles) + mine / p.box_tiles) * p.box_tiles) * 2048u;
+    // the word of piece c in the swizzled copy: 16-byte unit c ^ g of row g; bits 4-6 of the rest are 0
+    const uint32_t at = ring.base + box + (uint32_t)(swiglu ? in_box * 1024 : in_box * 2048) +
+                        (uint32_t)(g * 128 + t * 4 + (g << 4));
+    const uint32_t second = swiglu ? (uint32_t)p.box_tiles * 1024u : 1024u;
     uint32_t xr[NB];   // columns past the last pair repeat it; their results are not written
 #pragma unroll
-    for (int b = 0; b < NB; ++b) xr[b] = smem_u32(s_x) + min(b * 8 + g, cnt - 1) * p.x_stride + t * 16;
-    const uint32_t ring_at = smem_u32(ring) + at;
-    for (int m = 0, tile = first; m < mine; ++m, tile += step) {
+    for (int b = 0; b < NB; ++b) xr[b] = s_x + min(b * 8 + g, cnt - 1) * p.x_stride + t * 16;
+
+    // What a lane holds of a slice: the scales of the rows g and g + 8 for the 32-value pieces 2t and 2t + 1 (one scale
+    // for both with groups of 64 and more).  They come straight from global memory, a slice ahead, and are widened
+    // a slice later, so that nothing waits for them in between; their lines are brought into L2 a tile ahead.
+    // Past the last group nothing is read (a finite value stands there): x is zero, and so are the sums.
+    constexpr int kN = SHIFT == 5 ? 2 : 1, kPerChunk = kChunk >> SHIFT;
+    const Raw *sp0 = scales, *sp1 = scales;
+    uint32_t next[2 * kN] = {};
+    float s0[2 * kN];
+    auto scale_rows = [&](int tile) {
+        const int r = tile * rows_tile + g;
+        sp0 = scales + (int64_t)r * p.groups;
+        sp1 = r + half1 < p.n ? sp0 + (int64_t)half1 * p.groups : sp0;
+    };
+    auto load_scales = [&](int chunk) {
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+            const int q = chunk * kPerChunk + (((2 * t + j) * 32) >> SHIFT);
+            next[j] = next[kN + j] = 0;
+            if (q < p.groups) {
+                next[j] = __ldg(sp0 + q);
+                next[kN + j] = __ldg(sp1 + q);
+            }
+        }
+    };
+    auto prefetch_scales = [&](int tile) {
+        const int r = tile * rows_tile + (lane & 7) + (lane & 8 ? half1 : 0);
+        if (tile >= tile1 || r >= p.n) return;
+        const char *s = reinterpret_cast<const char *>(scales + (int64_t)r * p.groups);
+        for (int b = (lane >> 4) * 32; b < p.groups * (int)sizeof(Raw) + 31; b += 64)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(s + min(b, p.groups * (int)sizeof(Raw) - 1)));
+    };
+    if (tile0 + mine < tile1) {
+        scale_rows(tile0 + mine);
+        load_scales(share);
+    }
+    constexpr int kPieces = 1 << (SHIFT - 5);   // per scale: their products are added up before it is applied
+    for (int tile = tile0 + mine; tile - mine < tile1; tile += step) {
+        const bool have = tile < tile1;
         float acc[NB][4];
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[b][i] = 0.f;
-        for (int chunk = lo; chunk < hi && ok; ++chunk) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars[slot], (phases >> slot) & 1u, p.timeout_ns))) {
-                ok = false;   // the copies still in flight land before the block leaves
-                if (lane == 0)
-                    for (int i = 1, q = slot; i < flying; ++i) {
-                        if (++q == p.slots) q = 0;
-                        mbar_wait(&bars[q], (phases >> q) & 1u, p.timeout_ns);
-                    }
-                break;
-            }
-            phases ^= 1u << slot;
-            --flying;
-            load_scales();
-            const uint32_t box = ring_at + slot * kBoxBytes, x0 = chunk * (kChunk * 2);
-            float d[NB][4];
+        if (have) prefetch_scales(tile + step);
+        for (int j = 0; j < rounds; ++j) {
+            const int chunk = j * p.ks + share;
+            if (ring.ok)
+                ring.ok = __all_sync(0xffffffffu, mbar_wait(&ring.full[ring.slot], ring.phase, p.timeout_ns));
+            if (have && chunk < chunks && ring.ok) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const uint32_t w = box ^ (uint32_t)(c << 4);
-                uint32_t lo4[4], hi4[4];
-                decode8<FMT>(lds32(w), lo4);
-                decode8<FMT>(lds32(w + 1024), hi4);
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const uint4 xv = lds128(xr[b] + x0 + c * 64);
-                    if (c % kPieces == 0) mma16816_first(d[b], lo4[0], hi4[0], lo4[1], hi4[1], xv.x, xv.y);
-                    else mma16816(d[b], lo4[0], hi4[0], lo4[1], hi4[1], xv.x, xv.y);
-                    mma16816(d[b], lo4[2], hi4[2], lo4[3], hi4[3], xv.z, xv.w);
+                for (int i = 0; i < 2 * kN; ++i) s0[i] = wide_scale<FMT>(next[i]);
+                if (chunk + p.ks < chunks) {
+                    load_scales(chunk + p.ks);
+                } else if (tile + step < tile1) {
+                    scale_rows(tile + step);
+                    load_scales(share);
                 }
-                if (c % kPieces == kPieces - 1) {
-                    const float sa = __shfl_sync(0xffffffffu, s0[c % kN], (lane & ~3) | (c >> 1));
-                    const float sb = __shfl_sync(0xffffffffu, s0[kN + c % kN], (lane & ~3) | (c >> 1));
+                const uint32_t w0 = at + (uint32_t)ring.slot * kSlotBytes, x0 = (uint32_t)chunk * (kChunk * 2);
+                float d[NB][4];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint32_t w = w0 ^ (uint32_t)(c << 4);
+                    uint32_t lo4[4], hi4[4];
+                    decode8<FMT>(lds32(w), lo4);
+                    decode8<FMT>(lds32(w + second), hi4);
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
-                        acc[b][0] = fmaf(sa, d[b][0], acc[b][0]);
-                        acc[b][1] = fmaf(sa, d[b][1], acc[b][1]);
-                        acc[b][2] = fmaf(sb, d[b][2], acc[b][2]);
-                        acc[b][3] = fmaf(sb, d[b][3], acc[b][3]);
+                        const uint4 xv = lds128(xr[b] + x0 + c * 64);
+                        if (c % kPieces == 0) mma16816_first(d[b], lo4[0], hi4[0], lo4[1], hi4[1], xv.x, xv.y);
+                        else mma16816(d[b], lo4[0], hi4[0], lo4[1], hi4[1], xv.x, xv.y);
+                        mma16816(d[b], lo4[2], hi4[2], lo4[3], hi4[3], xv.z, xv.w);
+                    }
+                    if (c % kPieces == kPieces - 1) {
+                        const float sa = __shfl_sync(0xffffffffu, s0[c % kN], (lane & ~3) | (c >> 1));
+                        const float sb = __shfl_sync(0xffffffffu, s0[kN + c % kN], (lane & ~3) | (c >> 1));
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            acc[b][0] = fmaf(sa, d[b][0], acc[b][0]);
+                            acc[b][1] = fmaf(sa, d[b][1], acc[b][1]);
+                            acc[b][2] = fmaf(sb, d[b][2], acc[b][2]);
+                            acc[b][3] = fmaf(sb, d[b][3], acc[b][3]);
+                        }
                     }
                 }
             }
             __syncwarp();
-            if (in.left > 0) {
-                if (in.chunk == lo) prefetch_scales(in.tile);
-                if (lane == 0) issue(slot);
-                ++flying;
-                in.next(lo, hi, step);
+            if (lane == 0) mbar_arrive(&ring.empty[ring.slot]);
+            if (++ring.slot == p.slots) {
+                ring.slot = 0;
+                ring.phase ^= 1;
             }
-            take_scales();
-            if (++slot == p.slots) slot = 0;
         }
         if (p.ks > 1) {   // the shares of k are added in their order
             if (share > 0)
@@ -303,17 +290,17 @@ __device__ __forceinline__ bool run_tiles(const MatvecParams &p, const CUtensorM
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) part[warp][b * 4 + i][lane] = acc[b][i];
-            group_sync(1 + warp / p.ks, p.ks * 32);
+            group_sync(1 + mine, p.ks * 32);
             if (share == 0)
                 for (int s = 1; s < p.ks; ++s)
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) acc[b][i] += part[warp + s][b * 4 + i][lane];
-            group_sync(1 + warp / p.ks, p.ks * 32);
+            group_sync(1 + mine, p.ks * 32);
             if (share > 0) continue;
         }
-        if (!ok) continue;
+        if (!have || !ring.ok) continue;
         const int i0 = tile * rows_tile;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -341,51 +328,126 @@ __device__ __forceinline__ bool run_tiles(const MatvecParams &p, const CUtensorM
                 }
             }
     }
-    return ok;
 }
 
 template <int FMT, int SHIFT>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+__global__ void __launch_bounds__(kThreadsMv, 1)
     matvec_kernel(const __grid_constant__ CUtensorMap map, const MatvecParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = align_smem_1024(smem_raw);
-    __shared__ uint64_t s_bar[kWarps][kMaxSlots];
-    __shared__ uint32_t s_mask[kMaxExperts / 32];
-    __shared__ int s_live, s_cnt, s_bad;
+    __shared__ uint64_t s_full[kMaxSlots], s_empty[kMaxSlots];
+    __shared__ int s_count[kMaxExperts];             // pairs of each expert
+    __shared__ uint16_t s_experts[kMaxExperts];      // the experts that have a pair, ascending
+    __shared__ int64_t s_cost0[kMaxExperts + 1];     // cost before each of them
+    __shared__ int s_live, s_bad;
     __shared__ float s_part[kWarps][8][32];
-    __shared__ uint16_t s_experts[kMaxExperts];
-    uint8_t *s_x = smem + kWarps * p.slots * kBoxBytes;
+    uint8_t *s_x = smem + p.slots * kSlotBytes;
     uint16_t *s_list = reinterpret_cast<uint16_t *>(s_x + p.cols_pass * p.x_stride);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x < kWarps * kMaxSlots) mbar_init(&s_bar[threadIdx.x / kMaxSlots][threadIdx.x % kMaxSlots], 1);
-    fence_mbar_init();
-    if (threadIdx.x < kMaxExperts / 32) s_mask[threadIdx.x] = 0;
+    for (int i = threadIdx.x; i < kMaxExperts; i += kThreadsMv) s_count[i] = 0;
     if (threadIdx.x == 0) {
+        for (int i = 0; i < kMaxSlots; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_empty[i], kWarps);
+        }
+        fence_mbar_init();
         s_bad = 0;
         tma_prefetch_desc(&map);
     }
     __syncthreads();
     pdl_enter();
     const int pairs = (int)p.pairs;
-    for (int i = threadIdx.x; i < pairs; i += kWarps * 32) {
+    for (int i = threadIdx.x; i < pairs; i += kThreadsMv) {
         const int e = p.expert[i];
-        if (e >= 0 && e < p.N) atomicOr(&s_mask[e >> 5], 1u << (e & 31));
+        if (e >= 0 && e < p.N) atomicAdd(&s_count[e], 1);
         else s_bad = 1;
     }
     __syncthreads();
-    if (warp == 0) {   // the experts that have a pair, ascending
-        const uint32_t m = s_mask[lane];
-        int incl = __popc(m);
+    // lots of pairs that are staged together, and what a tile costs with them (a lot of more than 8 pairs: 5/4)
+    auto lots = [&](int e) { return (s_count[e] + p.cols_pass - 1) / p.cols_pass; };
+    auto tile_cost = [&](int e) {
+        const int full = s_count[e] / p.cols_pass, rest = s_count[e] % p.cols_pass;
+        return full * (p.cols_pass > 8 ? 5 : 4) + (rest > 8 ? 5 : rest > 0 ? 4 : 0);
+    };
+    if (warp == 0) {
+        int live = 0;
+        int64_t cost = 0;
+        for (int e0 = 0; e0 < p.N; e0 += 32) {
+            const int e = e0 + lane;
+            const bool has = e < p.N && s_count[e] > 0;
+            const uint32_t m = __ballot_sync(0xffffffffu, has);
+            if (m == 0) continue;
+            int64_t c = has ? (int64_t)tile_cost(e) * p.tiles : 0, incl = c;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += u;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += u;
+            }
+            if (has) {
+                const int at = live + __popc(m & ((1u << lane) - 1));
+                s_experts[at] = (uint16_t)e;
+                s_cost0[at] = cost + incl - c;
+            }
+            live += __popc(m);
+            cost += __shfl_sync(0xffffffffu, incl, 31);
         }
-        int at = incl - __popc(m);
-        for (uint32_t r = m; r; r &= r - 1) s_experts[at++] = (uint16_t)(lane * 32 + __ffs(r) - 1);
-        if (lane == 31) s_live = incl;
+        if (lane == 0) {
+            s_live = live;
+            s_cost0[live] = cost;
+        }
     }
     __syncthreads();
+    const int live = s_live;
+    // this block's share: the tiles whose cost starts in [x0, x1)
+    const int64_t x0 = s_cost0[live] * blockIdx.x / gridDim.x, x1 = s_cost0[live] * (blockIdx.x + 1) / gridDim.x;
+    int first = 0;
+    for (int hi = live - 1; first < hi;) {   // the last expert that starts at or before x0
+        const int mid = (first + hi + 1) >> 1;
+        if (s_cost0[mid] <= x0) first = mid;
+        else hi = mid - 1;
+    }
+    auto tile_at = [&](int y, int64_t x) {   // tiles of the y-th live expert that start before x
+        const int64_t c = s_cost0[y + 1] - s_cost0[y], per = c / p.tiles, d = x - s_cost0[y];
+        return d <= 0 ? 0 : (int)min((int64_t)p.tiles, (d + per - 1) / per);
+    };
+    const int step = kWarps / p.ks, chunks = (p.k + kChunk - 1) / kChunk, rounds = (chunks + p.ks - 1) / p.ks;
+    if (warp == kWarps) {
+        // ------------------------------------------------------------ copies
+        if (lane == 0) {
+            const int rows_tile = p.act == SWIGLU ? 8 : 16, boxes = step / p.box_tiles;
+            int slot = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            IssuedSlots iss;
+            for (int y = first; y < live && s_cost0[y] < x1 && ok; ++y) {
+                const int e = s_experts[y], tile0 = tile_at(y, x0), tile1 = tile_at(y, x1);
+                for (int lot = lots(e); lot > 0 && ok; --lot)
+                    for (int tile = tile0; tile < tile1 && ok; tile += step)
+                        for (int j = 0; j < rounds; ++j) {
+                            if (!mbar_wait(&s_empty[slot], phase ^ 1, p.timeout_ns)) {
+                                ok = false;
+                                break;
+                            }
+                            const int nb = min(boxes, (tile1 - tile + p.box_tiles - 1) / p.box_tiles);
+                            const int nk = min(p.ks, chunks - j * p.ks);
+                            mbar_arrive_expect_tx(&s_full[slot], (uint32_t)(nb * nk * p.box_tiles) * 2048u);
+                            for (int h = 0; h < nk; ++h)
+                                for (int b = 0; b < nb; ++b)
+                                    tma_load_codes(&map, &s_full[slot],
+                                                   smem + slot * kSlotBytes + (h * boxes + b) * p.box_tiles * 2048,
+                                                   (j * p.ks + h) * (kChunk / 2), (tile + b * p.box_tiles) * rows_tile, e);
+                            iss.note(slot, phase);
+                            if (++slot == p.slots) {
+                                slot = 0;
+                                phase ^= 1;
+                            }
+                        }
+            }
+            iss.drain(s_full, p.timeout_ns);   // every copy has landed before the block leaves
+        }
+        return;
+    }
+    // ---------------------------------------------------------------- products
     if (s_bad) {   // rows of pairs without an expert, shared by the blocks
         const int cols = p.act == SWIGLU ? p.n / 2 : p.n;
         for (int i = blockIdx.x; i < pairs; i += gridDim.x) {
@@ -398,34 +460,30 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             }
         }
     }
-    // this block's share of all live experts' tiles
-    const int64_t all = (int64_t)s_live * p.tiles;
-    const int64_t u0 = all * blockIdx.x / gridDim.x, u1 = all * (blockIdx.x + 1) / gridDim.x;
-    uint8_t *ring = smem + warp * p.slots * kBoxBytes;
-    uint32_t phases = 0;
-    int slot = 0;
-    bool ok = true;
-    for (int64_t u = u0; u < u1;) {
-        const int y = (int)(u / p.tiles), e = s_experts[y];
-        const int tile0 = (int)(u - (int64_t)y * p.tiles), tile1 = (int)min((int64_t)p.tiles, tile0 + (u1 - u));
-        __syncthreads();   // the last expert's list and rows of x have been used
+    constexpr int kAll = 15;   // named barrier of the consumer warps; the groups of a tile use 1..8
+    Ring ring;
+    ring.base = smem_u32(smem);
+    ring.full = s_full;
+    ring.empty = s_empty;
+    for (int y = first; y < live && s_cost0[y] < x1; ++y) {
+        const int e = s_experts[y], tile0 = tile_at(y, x0), tile1 = tile_at(y, x1);
+        if (tile0 >= tile1) continue;
+        if (y > first) group_sync(kAll, kWarps * 32);   // the last expert's list has been used
         if (warp == 0) {
             int cnt = 0;
             for (int i0 = 0; i0 < pairs; i0 += 32) {   // the expert's pairs in order
-                const bool mine = i0 + lane < pairs && p.expert[i0 + lane] == e;
-                const uint32_t b = __ballot_sync(0xffffffffu, mine);
-                if (mine) s_list[cnt + __popc(b & ((1u << lane) - 1))] = (uint16_t)(i0 + lane);
-                cnt += __popc(b);
+                const bool has = i0 + lane < pairs && p.expert[i0 + lane] == e;
+                const uint32_t m = __ballot_sync(0xffffffffu, has);
+                if (has) s_list[cnt + __popc(m & ((1u << lane) - 1))] = (uint16_t)(i0 + lane);
+                cnt += __popc(m);
             }
-            if (lane == 0) s_cnt = cnt;
         }
-        __syncthreads();
         // as many pairs at a time as are staged; the weights are read again (from L2) for each lot
-        for (int c = 0; c < s_cnt; c += p.cols_pass) {
-            const int cnt = min(s_cnt - c, p.cols_pass);
-            if (c > 0) __syncthreads();
+        for (int c = 0; c < s_count[e]; c += p.cols_pass) {
+            const int cnt = min(s_count[e] - c, p.cols_pass);
+            group_sync(kAll, kWarps * 32);   // the list is there; the rows of x before have been used
             // x as 16-byte pieces (8 values of a lane), each as the pairs (0, 4), (1, 5), (2, 6), (3, 7); zeros from k
-            // to the end of the last chunk
+            // to the end of the last slice
             const int pieces = (int)(p.x_stride / 16);
             for (int i = threadIdx.x; i < cnt * pieces; i += kWarps * 32) {
                 const int col = i / pieces, q = i - col * pieces;
@@ -436,12 +494,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
                                __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
             }
-            ok = cnt <= 8 ? run_tiles<FMT, SHIFT, 1>(p, &map, ring, s_bar[warp], phases, slot, s_x, s_part, e, tile0,
-                                                     tile1, s_list + c, cnt, ok)
-                          : run_tiles<FMT, SHIFT, 2>(p, &map, ring, s_bar[warp], phases, slot, s_x, s_part, e, tile0,
-                                                     tile1, s_list + c, cnt, ok);
+            group_sync(kAll, kWarps * 32);
+            if (cnt <= 8) run_tiles<FMT, SHIFT, 1>(p, ring, smem_u32(s_x), s_part, e, tile0, tile1, s_list + c, cnt);
+            else run_tiles<FMT, SHIFT, 2>(p, ring, smem_u32(s_x), s_part, e, tile0, tile1, s_list + c, cnt);
         }
-        u += tile1 - tile0;
     }
 }
 
@@ -449,7 +505,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 // of two rows hit different banks.
 constexpr uint32_t x_stride(int k) { return (uint32_t)((k + kChunk - 1) / kChunk * kChunk * 2 + 64); }
 constexpr size_t matvec_smem(int slots, int cols, int k, int64_t pairs) {
-    return 1024 + (size_t)kWarps * slots * kBoxBytes + (size_t)cols * x_stride(k) + (size_t)pairs * 2;
+    return 1024 + (size_t)slots * kSlotBytes + (size_t)cols * x_stride(k) + (size_t)pairs * 2;
 }
 
 // Codes and scales of fp32 or bf16 weights: one warp per group of values.
