@@ -98,22 +98,34 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
     return d;
 }
 
+// A constant that stays in a register: left to itself the compiler loads it again at every use.
+__device__ __forceinline__ uint32_t held(uint32_t v) {
+    uint32_t r;
+    asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+template <int FMT>
+struct Magic {
+    // int4: 0x4300 | c is the bf16 128 + c, and 136 to take off.  e2m1: the sign's place, and 2^126.
+    uint32_t a = held(FMT == INT4 ? 0x43004300u : 0x80008000u), b = held(FMT == INT4 ? 0x43084308u : 0x7e807e80u);
+};
+
 // 8 codes as four bf16 pairs (i, i + 4), i = 0..3.
 template <int FMT>
-__device__ __forceinline__ void decode8(uint32_t w, uint32_t (&v)[4]) {
+__device__ __forceinline__ void decode8(uint32_t w, const Magic<FMT> &m, uint32_t (&v)[4]) {
     if (FMT == INT4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {   // 0x4300 | c is 128 + c; minus 136 exactly c - 8
-            v[i] = and_or(w >> (4 * i), 0x000f000fu, 0x43004300u);
-            asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(v[i]) : "r"(0x43084308u));
+        for (int i = 0; i < 4; ++i) {   // 128 + c - 136, exactly
+            v[i] = and_or(w >> (4 * i), 0x000f000fu, m.a);
+            asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(v[i]) : "r"(m.b));
         }
     } else {
         // exponent and mantissa bits at bf16's place read as value 2^-126 (subnormals included); times 2^126 exactly
-        const uint32_t m[4] = {w << 6, w << 2, w >> 2, w >> 6}, s[4] = {w << 12, w << 8, w << 4, w};
+        const uint32_t e[4] = {w << 6, w << 2, w >> 2, w >> 6}, s[4] = {w << 12, w << 8, w << 4, w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[i] = and_or(m[i], 0x01c001c0u, s[i] & 0x80008000u);
-            asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v[i]) : "r"(0x7e807e80u));
+            v[i] = and_or(e[i], 0x01c001c0u, s[i] & m.a);
+            asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v[i]) : "r"(m.b));
         }
     }
 }
@@ -227,6 +239,7 @@ __device__ __forceinline__ void run_tiles(const MatvecParams &p, Ring &ring, uin
         scale_rows(tile0 + mine);
         load_scales(share);
     }
+    const Magic<FMT> magic;
     constexpr int kPieces = 1 << (SHIFT - 5);   // per scale: their products are added up before it is applied
     for (int tile = tile0 + mine; tile - mine < tile1; tile += step) {
         const bool have = tile < tile1;
@@ -251,15 +264,25 @@ __device__ __forceinline__ void run_tiles(const MatvecParams &p, Ring &ring, uin
                 }
                 const uint32_t w0 = at + (uint32_t)ring.slot * kSlotBytes, x0 = (uint32_t)chunk * (kChunk * 2);
                 float d[NB][4];
+                // the whole slice's codes and the next piece's x are read ahead of their use
+                uint32_t wl[8], wh[8];
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    const uint32_t w = w0 ^ (uint32_t)(c << 4);
+                    wl[c] = lds32(w0 ^ (uint32_t)(c << 4));
+                    wh[c] = lds32((w0 ^ (uint32_t)(c << 4)) + second);
+                }
+                uint4 xn[NB];
+#pragma unroll
+                for (int b = 0; b < NB; ++b) xn[b] = lds128(xr[b] + x0);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
                     uint32_t lo4[4], hi4[4];
-                    decode8<FMT>(lds32(w), lo4);
-                    decode8<FMT>(lds32(w + second), hi4);
+                    decode8<FMT>(wl[c], magic, lo4);
+                    decode8<FMT>(wh[c], magic, hi4);
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
-                        const uint4 xv = lds128(xr[b] + x0 + c * 64);
+                        const uint4 xv = xn[b];
+                        if (c < 7) xn[b] = lds128(xr[b] + x0 + (c + 1) * 64);
                         if (c % kPieces == 0) mma16816_first(d[b], lo4[0], hi4[0], lo4[1], hi4[1], xv.x, xv.y);
                         else mma16816(d[b], lo4[0], hi4[0], lo4[1], hi4[1], xv.x, xv.y);
                         mma16816(d[b], lo4[2], hi4[2], lo4[3], hi4[3], xv.z, xv.w);
@@ -343,6 +366,7 @@ __global__ void __launch_bounds__(kThreadsMv, 1)
     __shared__ float s_part[kWarps][8][32];
     uint8_t *s_x = smem + p.slots * kSlotBytes;
     uint16_t *s_list = reinterpret_cast<uint16_t *>(s_x + p.cols_pass * p.x_stride);
+    int16_t *s_expert = reinterpret_cast<int16_t *>(s_list + p.pairs);   // each pair's expert, -1: none
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i < kMaxExperts; i += kThreadsMv) s_count[i] = 0;
     if (threadIdx.x == 0) {
@@ -359,8 +383,10 @@ __global__ void __launch_bounds__(kThreadsMv, 1)
     const int pairs = (int)p.pairs;
     for (int i = threadIdx.x; i < pairs; i += kThreadsMv) {
         const int e = p.expert[i];
-        if (e >= 0 && e < p.N) atomicAdd(&s_count[e], 1);
+        const bool good = e >= 0 && e < p.N;
+        if (good) atomicAdd(&s_count[e], 1);
         else s_bad = 1;
+        s_expert[i] = good ? (int16_t)e : (int16_t)-1;
     }
     __syncthreads();
     // lots of pairs that are staged together, and what a tile costs with them (a lot of more than 8 pairs: 5/4)
@@ -472,7 +498,7 @@ __global__ void __launch_bounds__(kThreadsMv, 1)
         if (warp == 0) {
             int cnt = 0;
             for (int i0 = 0; i0 < pairs; i0 += 32) {   // the expert's pairs in order
-                const bool has = i0 + lane < pairs && p.expert[i0 + lane] == e;
+                const bool has = i0 + lane < pairs && s_expert[i0 + lane] == e;
                 const uint32_t m = __ballot_sync(0xffffffffu, has);
                 if (has) s_list[cnt + __popc(m & ((1u << lane) - 1))] = (uint16_t)(i0 + lane);
                 cnt += __popc(m);
@@ -484,15 +510,25 @@ __global__ void __launch_bounds__(kThreadsMv, 1)
             group_sync(kAll, kWarps * 32);   // the list is there; the rows of x before have been used
             // x as 16-byte pieces (8 values of a lane), each as the pairs (0, 4), (1, 5), (2, 6), (3, 7); zeros from k
             // to the end of the last slice
-            const int pieces = (int)(p.x_stride / 16);
-            for (int i = threadIdx.x; i < cnt * pieces; i += kWarps * 32) {
-                const int col = i / pieces, q = i - col * pieces;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (q * 8 < p.k)
-                    v = __ldg(reinterpret_cast<const uint4 *>(p.x + (int64_t)(s_list[c + col] / p.x_div) * p.k) + q);
-                *reinterpret_cast<uint4 *>(s_x + col * p.x_stride + q * 16) =
-                    make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                               __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+            const int pieces = (int)(p.x_stride / 16), total = cnt * pieces;
+            constexpr int kAhead = 4;   // loads in flight per thread
+            for (int i0 = threadIdx.x; i0 < total; i0 += kAhead * kWarps * 32) {
+                uint4 v[kAhead];
+                uint32_t dst[kAhead];
+#pragma unroll
+                for (int a = 0; a < kAhead; ++a) {
+                    const int i = i0 + a * kWarps * 32, col = min(i, total - 1) / pieces, q = min(i, total - 1) - col * pieces;
+                    dst[a] = col * p.x_stride + q * 16;
+                    v[a] = make_uint4(0, 0, 0, 0);
+                    if (i < total && q * 8 < p.k)
+                        v[a] = __ldg(reinterpret_cast<const uint4 *>(p.x + (int64_t)(s_list[c + col] / p.x_div) * p.k) + q);
+                }
+#pragma unroll
+                for (int a = 0; a < kAhead; ++a)
+                    if (i0 + a * kWarps * 32 < total)
+                        *reinterpret_cast<uint4 *>(s_x + dst[a]) =
+                            make_uint4(__byte_perm(v[a].x, v[a].z, 0x5410), __byte_perm(v[a].x, v[a].z, 0x7632),
+                                       __byte_perm(v[a].y, v[a].w, 0x5410), __byte_perm(v[a].y, v[a].w, 0x7632));
             }
             group_sync(kAll, kWarps * 32);
             if (cnt <= 8) run_tiles<FMT, SHIFT, 1>(p, ring, smem_u32(s_x), s_part, e, tile0, tile1, s_list + c, cnt);
@@ -505,7 +541,7 @@ __global__ void __launch_bounds__(kThreadsMv, 1)
 // of two rows hit different banks.
 constexpr uint32_t x_stride(int k) { return (uint32_t)((k + kChunk - 1) / kChunk * kChunk * 2 + 64); }
 constexpr size_t matvec_smem(int slots, int cols, int k, int64_t pairs) {
-    return 1024 + (size_t)slots * kSlotBytes + (size_t)cols * x_stride(k) + (size_t)pairs * 2;
+    return 1024 + (size_t)slots * kSlotBytes + (size_t)cols * x_stride(k) + (size_t)pairs * 4;
 }
 
 // Codes and scales of fp32 or bf16 weights: one warp per group of values.
