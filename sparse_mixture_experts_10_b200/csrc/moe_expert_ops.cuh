@@ -123,7 +123,9 @@ int launch_gmm_tc(gmm::Params p, const DeviceInfo &dev, cudaStream_t s) {
     // row tiles there are at least (segments are on the device; this is what the host knows)
     auto row_tiles = [&](int64_t unit) { return std::max(live, cdiv(p.rows, unit)); };
     const bool pair = (KIND == gmm::TN ? p.G * cdiv(p.n, 256) : row_tiles(256)) * cdiv(F, 256) >= dev.pair_clusters;
-    const bool wide = pair && KIND != gmm::TN && p.rows > 256 * live && row_tiles(512) * cdiv(F, 256) >= dev.pair_clusters;
+    // tiles of up to 512 rows need both accumulators, and no registers hold an fp32 result's running sums of them
+    const bool wide = pair && KIND != gmm::TN && sizeof(TO) == 2 && p.rows > 256 * live &&
+                      row_tiles(512) * cdiv(F, 256) >= dev.pair_clusters;
     const int unit = pair ? 256 : 128;
     p.m_tiles = (int)cdiv(F, unit);
     p.n_tiles = (int)cdiv(p.n, unit);
@@ -134,7 +136,7 @@ int launch_gmm_tc(gmm::Params p, const DeviceInfo &dev, cudaStream_t s) {
     const size_t smem = gmm::tc_smem_bytes(p.G);
     if (pair) {
         const dim3 grid((unsigned)(2 * std::min<int64_t>(upper, dev.pair_clusters)));
-        if constexpr (KIND != gmm::TN)
+        if constexpr (KIND != gmm::TN && sizeof(TO) == 2)
             if (wide)
                 return launch_pdl(gmm::tc_pair_kernel<KIND, TO, true>, grid, dim3(gmm::kTcThreads), smem, s, mm, mn, p);
         return launch_pdl(gmm::tc_pair_kernel<KIND, TO, false>, grid, dim3(gmm::kTcThreads), smem, s, mm, mn, p);
@@ -272,9 +274,7 @@ int expert_ops_attrs() {
     MOE_GMM_ATTR(gmm::NT);
     MOE_GMM_ATTR(gmm::NN);
     MOE_GMM_ATTR(gmm::TN);
-    MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NT, float, true>));
     MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NT, __nv_bfloat16, true>));
-    MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NN, float, true>));
     MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NN, __nv_bfloat16, true>));
 #undef MOE_GMM_ATTR
     MOE_TRY(allow_smem(q4::matvec_kernel<q4::INT4, 5>));

@@ -15,13 +15,13 @@
 //
 // One persistent CTA (kPair false: tiles of 128 x <=128) or CTA pair (tiles of
 // 256 x <=256, each CTA of the pair loads its 128 f's and half of the rows)
-// per SM; 352 threads:
-//   warps 0-7  epilogue: tcgen05.ld 32 columns at a time; a lane holds one f,
+// per SM:
+//   epilogue   16 warps: tcgen05.ld; a lane holds one f,
 //              so a warp writes 32 consecutive values of a row (bf16: two
 //              rows of pairs after a lane exchange)
-//   warp 8     TMA producer: 64-wide slices along c into a ring
-//   warp 9     issues tcgen05.mma into one of two accumulators
-//   warp 10    TN: clears the rows behind a segment's end in its last slice.
+//   producer   one warp: TMA copies of 64-wide slices along c into a ring
+//   issuer     one warp: tcgen05.mma into one of two accumulators
+//   clearer    one warp, TN: clears the rows behind a segment's end in its last slice.
 //              Those rows belong to another expert (or to nobody) and may hold
 //              anything, NaN included, so both operands are cleared
 // Slices past the end of n or k are zero-filled by TMA: the weights' tensor map
@@ -41,7 +41,22 @@ namespace gmm {
 
 constexpr int kSl = 64;                 // slice along the contraction
 constexpr int kOpBytes = 128 * kSl * 2; // 128 values of either side of a slice
-constexpr int kTcThreads = 32 * 11;
+// 16 epilogue warps: a weight gradient over few rows is mostly its epilogue (18 gradients of 4096 x 2048 over 512
+// rows each: 208 us with 8 warps, 167 us with 16).
+constexpr int kEpi = 16;
+constexpr int kTcThreads = 32 * (kEpi + 3);
+// The tensor core's fp32 accumulation drops what is behind the last bit, always towards zero: measured against 64
+// bits, the result comes out small by 8e-10 of itself for every term (4.4e-6 after 4096, 1.9e-5 after 16384).
+// A bf16 result (2^-9) does not show it.  For an fp32 result the contraction is cut into equal runs of at most 12
+// slices (768 terms, 6e-7); the accumulator is read after each and added, rounded to nearest, to running sums in
+// registers.
+constexpr int kRun = 12;
+template <bool kF32>
+__device__ __forceinline__ int run_length(int nkb) {
+    if (!kF32 || nkb <= kRun) return nkb;
+    const int runs = (nkb + kRun - 1) / kRun;
+    return (nkb + runs - 1) / runs;
+}
 constexpr int kMaxStages = 6;
 
 // Slices in the ring: 192 KB of shared memory either way.
@@ -179,35 +194,30 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const int *s_off, const
     return t;
 }
 
-// 32 accumulator columns (rows r0.. of the result) of this lane's f.
-template <typename TO>
-__device__ __forceinline__ void store_cols(TO *out, int64_t ldc, int f, bool f_ok, const uint32_t (&r)[32], int rows,
-                                           int accumulate) {
-    if (sizeof(TO) == 4) {
-        float *dst = reinterpret_cast<float *>(out) + f;
+// N accumulator columns (rows of the result) of this lane's f; rows: how many of them there are.
+template <int N>
+__device__ __forceinline__ void store_f32(float *dst, int64_t ldc, bool f_ok, const float (&v)[N], int rows,
+                                          int accumulate) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            if (j < rows && f_ok) {
-                const float v = __uint_as_float(r[j]);
-                dst[j * ldc] = accumulate ? dst[j * ldc] + v : v;
-            }
-        }
-    } else {
-        const int odd = threadIdx.x & 1;
-        __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(out) + (f & ~1) + (odd ? ldc : 0);
+    for (int j = 0; j < N; ++j)
+        if (j < rows && f_ok) dst[j * ldc] = accumulate ? dst[j * ldc] + v[j] : v[j];
+}
+__device__ __forceinline__ void store_bf16(__nv_bfloat16 *out, int64_t ldc, int f, bool f_ok, const uint32_t (&r)[32],
+                                           int rows, int accumulate) {
+    const int odd = threadIdx.x & 1;
+    __nv_bfloat16 *dst = out + (f & ~1) + (odd ? ldc : 0);
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {   // even lanes write row j, odd lanes row j + 1
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? r[j] : r[j + 1], 1);
-            float lo = __uint_as_float(odd ? got : r[j]), hi = __uint_as_float(odd ? r[j + 1] : got);
-            if (j + odd < rows && f_ok) {
-                uint32_t *q = reinterpret_cast<uint32_t *>(dst + j * ldc);
-                if (accumulate) {
-                    const uint32_t o = *q;
-                    lo += __uint_as_float(o << 16);
-                    hi += __uint_as_float(o & 0xffff0000u);
-                }
-                *q = pack_bf16x2(lo, hi);
+    for (int j = 0; j < 32; j += 2) {   // even lanes write row j, odd lanes row j + 1
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? r[j] : r[j + 1], 1);
+        float lo = __uint_as_float(odd ? got : r[j]), hi = __uint_as_float(odd ? r[j + 1] : got);
+        if (j + odd < rows && f_ok) {
+            uint32_t *q = reinterpret_cast<uint32_t *>(dst + j * ldc);
+            if (accumulate) {
+                const uint32_t o = *q;
+                lo += __uint_as_float(o << 16);
+                hi += __uint_as_float(o & 0xffff0000u);
             }
+            *q = pack_bf16x2(lo, hi);
         }
     }
 }
@@ -215,7 +225,8 @@ __device__ __forceinline__ void store_cols(TO *out, int64_t ldc, int f, bool f_o
 template <int KIND, typename TO, bool kPair, bool kWide>
 __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN, const Params &p) {
     pdl_enter();
-    static_assert(!kWide || (kPair && KIND != TN), "wide tiles: CTA pairs, K-major N operand");
+    constexpr bool kF32 = sizeof(TO) == 4;
+    static_assert(!kWide || (kPair && KIND != TN && !kF32), "wide tiles: CTA pairs, K-major N operand, bf16 results");
     constexpr int kAccCols = kPair ? 256 : 128;
     constexpr int kStages = ring_stages(kWide), kNBytes = (kWide ? 2 : 1) * kOpBytes;
     constexpr bool kMmn = KIND != NT, kNmn = KIND == TN;   // MN-major operands
@@ -238,7 +249,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
     const int step = kPair ? (int)tc::nclusters_x() : (int)gridDim.x;
 
     if (warp == 0) load_segments(p.row_offsets, p.G, p.rows, (kWide ? 2 : 1) * kAccCols, s_off, s_cum);
-    if (warp == 8 && lane == 0) {
+    if (warp == kEpi && lane == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
@@ -247,7 +258,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&tfull[a], 1);
-            mbar_init(&tempty[a], (kPair ? 2 : 1) * 8);
+            mbar_init(&tempty[a], (kPair ? 2 : 1) * kEpi);
         }
         mbar_init(drain, 1);
         fence_mbar_init();
@@ -255,7 +266,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
         tma_prefetch_desc(&tmN.m[0]);
         if (!kNmn) tma_prefetch_desc(&tmN.m[7]);
     }
-    if (warp == 9) {
+    if (warp == kEpi + 1) {
         if (kPair) tc::tmem_alloc2(tmem_slot, 2 * kAccCols);
         else tmem_alloc(tmem_slot, 2 * kAccCols);
     }
@@ -267,7 +278,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
     const int total = KIND == TN ? p.total : s_cum[p.G] * p.m_tiles;
     auto tile = [&](int i) { return tile_at<KIND, kPair, kWide>(p, s_off, s_cum, i); };
 
-    if (warp == 8) {
+    if (warp == kEpi) {
         // ------------------------------------------------------------ TMA producer
         int stage = 0;
         uint32_t phase = 0;
@@ -302,7 +313,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
                         if (kWide && t.nsub == 2) tma_load_3d<P>(mapN, bar, dN + kOpBytes, c, r + t.nh, 0);
                     }
                 };
-                if (KIND == TN && kb == nkb - 1 && t.nc % kSl != 0) {   // warp 10 passes it on
+                if (KIND == TN && kb == nkb - 1 && t.nc % kSl != 0) {   // the clearer passes it on
                     if (elect_one()) {
                         mbar_arrive_expect_tx(&raw[stage], bytes);
                         loads(std::false_type{}, smem_u32(&raw[stage]));
@@ -328,7 +339,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
             iss_raw.drain(raw, p.timeout_ns);
             if (rank == 0) iss.drain(full, p.timeout_ns);
         }
-    } else if (warp == 9) {
+    } else if (warp == kEpi + 1) {
         // ------------------------------------------------------------ MMA issuer (leader CTA)
         if (rank == 0) {
             constexpr uint32_t kIdesc = idesc_bf16_f32(kPair ? 256 : 128, 0) | (kMmn ? 1u << 15 : 0u) |
@@ -340,54 +351,61 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
             for (int i = first; i < total && ok; i += step) {
                 const Tile t = tile(i);
                 if (KIND == TN ? t.nc == 0 : t.rows <= 0) continue;
-                const int a0 = kWide ? 0 : local & 1;
-                ++local;
                 const uint32_t idesc = kIdesc | (static_cast<uint32_t>(t.nh >> 3) << 17);
                 const int nkb = (t.nc + kSl - 1) / kSl;
-                const uint32_t d_tmem = tmem_base + a0 * kAccCols;
-                for (int a = a0; a < a0 + t.nsub && ok; ++a) {   // the accumulators have been read
-                    const uint32_t ph = (acc_phase >> a) & 1u;
-                    ok = __all_sync(0xffffffffu, kPair ? tc::mbar_wait_cluster(&tempty[a], ph, p.timeout_ns)
-                                                       : mbar_wait(&tempty[a], ph, p.timeout_ns));
-                    acc_phase ^= 1u << a;
-                }
-                for (int kb = 0; kb < nkb && ok; ++kb) {
-                    if (KIND == TN && kb == nkb - 1 && t.nc % kSl != 0) {   // written by threads too, maybe the other CTA's
-                        const uint32_t ph = (fixed_phase >> stage) & 1u;
-                        ok = __all_sync(0xffffffffu, kPair ? tc::mbar_wait_cluster(&fixed[stage], ph, p.timeout_ns)
-                                                           : mbar_wait(&fixed[stage], ph, p.timeout_ns));
-                        fixed_phase ^= 1u << stage;
-                    } else {
-                        ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], (full_phase >> stage) & 1u, p.timeout_ns));
-                        full_phase ^= 1u << stage;
+                const int run = run_length<kF32>(nkb);
+                for (int kb = 0, end = 0; kb < nkb && ok;) {
+                    end = min(nkb, kb + run);
+                    const int a0 = kWide ? 0 : local & 1;
+                    ++local;
+                    const uint32_t d_tmem = tmem_base + a0 * kAccCols;
+                    for (int a = a0; a < a0 + t.nsub && ok; ++a) {   // the accumulators have been read
+                        const uint32_t ph = (acc_phase >> a) & 1u;
+                        ok = __all_sync(0xffffffffu, kPair ? tc::mbar_wait_cluster(&tempty[a], ph, p.timeout_ns)
+                                                           : mbar_wait(&tempty[a], ph, p.timeout_ns));
+                        acc_phase ^= 1u << a;
                     }
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t aM = smem_u32(sM + stage * kOpBytes), aN = smem_u32(sN + stage * kNBytes);
-                    const uint64_t dm = kMmn ? smem_desc_mn(aM) : smem_desc_sw128(aM);
-                    const uint64_t dn = kNmn ? smem_desc_mn(aN) : smem_desc_sw128(aN);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < kSl / 16; ++k) {
-                            const uint64_t m = dm + (kMmn ? 128 : 2) * k, n = dn + (kNmn ? 128 : 2) * k;
-                            const uint32_t acc = (kb | k) != 0 ? 1u : 0u;
-                            if (kPair) tc::tc_mma2_bf16(d_tmem, m, n, idesc, acc);
-                            else tc_mma_bf16(d_tmem, m, n, idesc, acc);
-                            // the two accumulators in turn, so that an instruction does not wait for the one before it
-                            if (kWide && t.nsub == 2)
-                                tc::tc_mma2_bf16(d_tmem + kAccCols, m, n + (kOpBytes >> 4), idesc, acc);
+                    uint32_t acc = 0;
+                    for (; kb < end && ok; ++kb) {
+                        if (KIND == TN && kb == nkb - 1 && t.nc % kSl != 0) {   // written by threads too, maybe the other CTA's
+                            const uint32_t ph = (fixed_phase >> stage) & 1u;
+                            ok = __all_sync(0xffffffffu, kPair ? tc::mbar_wait_cluster(&fixed[stage], ph, p.timeout_ns)
+                                                               : mbar_wait(&fixed[stage], ph, p.timeout_ns));
+                            fixed_phase ^= 1u << stage;
+                        } else {
+                            ok = __all_sync(0xffffffffu,
+                                            mbar_wait(&full[stage], (full_phase >> stage) & 1u, p.timeout_ns));
+                            full_phase ^= 1u << stage;
                         }
-                        if (kPair) tc::tc_commit2_mc(&empty[stage], 0x3);
-                        else tc_commit(&empty[stage]);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t aM = smem_u32(sM + stage * kOpBytes), aN = smem_u32(sN + stage * kNBytes);
+                        const uint64_t dm = kMmn ? smem_desc_mn(aM) : smem_desc_sw128(aM);
+                        const uint64_t dn = kNmn ? smem_desc_mn(aN) : smem_desc_sw128(aN);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < kSl / 16; ++k) {
+                                const uint64_t m = dm + (kMmn ? 128 : 2) * k, n = dn + (kNmn ? 128 : 2) * k;
+                                if (kPair) tc::tc_mma2_bf16(d_tmem, m, n, idesc, acc);
+                                else tc_mma_bf16(d_tmem, m, n, idesc, acc);
+                                // the two accumulators in turn, so that an instruction does not wait for the one before it
+                                if (kWide && t.nsub == 2)
+                                    tc::tc_mma2_bf16(d_tmem + kAccCols, m, n + (kOpBytes >> 4), idesc, acc);
+                                acc = 1;
+                            }
+                            if (kPair) tc::tc_commit2_mc(&empty[stage], 0x3);
+                            else tc_commit(&empty[stage]);
+                        }
+                        acc = 1;
+                        __syncwarp();
+                        if (++stage == kStages) stage = 0;
+                    }
+                    if (ok && elect_one()) {
+                        if (kPair) tc::tc_commit2_mc(&tfull[a0], 0x3);
+                        else tc_commit(&tfull[a0]);
                     }
                     __syncwarp();
-                    if (++stage == kStages) stage = 0;
                 }
-                if (ok && elect_one()) {
-                    if (kPair) tc::tc_commit2_mc(&tfull[a0], 0x3);
-                    else tc_commit(&tfull[a0]);
-                }
-                __syncwarp();
             }
             if (!ok) {   // wait (bounded) for the MMAs already issued before TMEM is freed
                 if (elect_one()) {
@@ -398,7 +416,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
                 mbar_wait(drain, 0, p.timeout_ns);
             }
         }
-    } else if (warp == 10) {
+    } else if (warp == kEpi + 2) {
         // ------------------------------------------------------------ TN: rows behind the segment's end
         if (KIND == TN) {
             int it = 0;
@@ -437,30 +455,68 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
             TO *out = static_cast<TO *>(p.C) + ((KIND == TN ? (int64_t)t.g * p.n : 0) + t.r0) * p.ldc;
             if (KIND == TN && t.nc == 0) {   // an expert without rows: its gradient is zero
                 if (!p.accumulate && f_ok)
-                    for (int j = part; j < t.rows; j += 2) out[j * p.ldc + f] = TO(0.0f);
+                    for (int j = part; j < t.rows; j += kEpi / 4) out[j * p.ldc + f] = TO(0.0f);
                 continue;
             }
-            const int a0 = kWide ? 0 : local & 1;
-            const uint32_t ph = kWide ? local & 1 : (local >> 1) & 1;
-            ++local;
-            // warp-uniform decision: the TMEM loads below are warp-collective
-            if (!__all_sync(0xffffffffu, mbar_wait(&tfull[a0], ph, p.timeout_ns))) break;
-            tc_fence_after();
-            for (int h = 0; h < t.nsub; ++h) {
-                const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (a0 + h) * kAccCols;
-                const int rows = min(t.nh, t.rows - h * t.nh);
-                TO *dst = out + (int64_t)h * t.nh * p.ldc;
-                for (int c = part * 32; c < rows; c += 64) {
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(tb + c, r);
-                    tmem_ld_wait();
-                    store_cols(dst + c * p.ldc, p.ldc, f, f_ok, r, rows - c, KIND == TN ? p.accumulate : 0);
-                }
+            auto release = [&](int a) {   // the accumulator has been read
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (kPair) mbar_arrive_remote_relaxed(tc::mapa_shared(smem_u32(&tempty[a0 + h]), 0));
-                    else mbar_arrive(&tempty[a0 + h]);
+                    if (kPair) mbar_arrive_remote_relaxed(tc::mapa_shared(smem_u32(&tempty[a]), 0));
+                    else mbar_arrive(&tempty[a]);
+                }
+            };
+            const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+            if constexpr (kF32) {
+                // running sums of this warp's columns
+                constexpr int kCols = kAccCols / 4, kC16 = kCols / 16;
+                const int c0 = part * kCols, nkb = (t.nc + kSl - 1) / kSl, run = run_length<kF32>(nkb);
+                float sum[kC16][16];
+#pragma unroll
+                for (int c = 0; c < kC16; ++c)
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) sum[c][k] = 0.f;
+                bool ok = true;
+                for (int kb = 0; kb < nkb && ok; kb += run) {
+                    const int a = local & 1;
+                    const uint32_t ph = (local >> 1) & 1;
+                    ++local;
+                    // warp-uniform decision: the TMEM loads below are warp-collective
+                    ok = __all_sync(0xffffffffu, mbar_wait(&tfull[a], ph, p.timeout_ns));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < kC16; ++c) {
+                        if (c0 + c * 16 >= t.rows) break;   // warp-uniform
+                        uint32_t r[16];
+                        tc::tmem_ld_32x32b_x16(lanes + a * kAccCols + c0 + c * 16, r);
+                        tc::tmem_ld_wait_regs(r);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) sum[c][k] += __uint_as_float(r[k]);
+                    }
+                    release(a);
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int c = 0; c < kC16; ++c)
+                    store_f32<16>(out + (c0 + c * 16) * p.ldc + f, p.ldc, f_ok, sum[c], t.rows - c0 - c * 16,
+                                  KIND == TN ? p.accumulate : 0);
+            } else {
+                const int a0 = kWide ? 0 : local & 1;
+                const uint32_t ph = kWide ? local & 1 : (local >> 1) & 1;
+                ++local;
+                if (!__all_sync(0xffffffffu, mbar_wait(&tfull[a0], ph, p.timeout_ns))) break;
+                tc_fence_after();
+                for (int h = 0; h < t.nsub; ++h) {
+                    const int rows = min(t.nh, t.rows - h * t.nh);
+                    TO *dst = out + (int64_t)h * t.nh * p.ldc;
+                    for (int c = part * 32; c < rows; c += 32 * (kEpi / 4)) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(lanes + (a0 + h) * kAccCols + c, r);
+                        tmem_ld_wait();
+                        store_bf16(dst + c * p.ldc, p.ldc, f, f_ok, r, rows - c, KIND == TN ? p.accumulate : 0);
+                    }
+                    release(a0 + h);
                 }
             }
         }
@@ -468,7 +524,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
     tc_fence_before();
     __syncthreads();
     if (kPair) tc::cluster_sync();   // the leader's last MMAs read this CTA's shared memory and TMEM
-    if (warp == 9) {
+    if (warp == kEpi + 1) {
         tc_fence_after();
         if (kPair) tc::tmem_dealloc2(tmem_base, 2 * kAccCols);
         else tmem_dealloc(tmem_base, 2 * kAccCols);
