@@ -21,9 +21,10 @@
 //              rows of pairs after a lane exchange)
 //   producer   one warp: TMA copies of 64-wide slices along c into a ring
 //   issuer     one warp: tcgen05.mma into one of two accumulators
-//   clearer    one warp, TN: clears the rows behind a segment's end in its last slice.
-//              Those rows belong to another expert (or to nobody) and may hold
-//              anything, NaN included, so both operands are cleared
+//   clearer    one warp, TN: clears the rows behind a segment's end in its last
+//              slice, up to the next 16 (further steps of the slice are not
+//              issued).  Those rows belong to another expert (or to nobody) and
+//              may hold anything, NaN included, so both operands are cleared
 // Slices past the end of n or k are zero-filled by TMA: the weights' tensor map
 // has the group as its own dimension.
 //
@@ -313,7 +314,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
                         if (kWide && t.nsub == 2) tma_load_3d<P>(mapN, bar, dN + kOpBytes, c, r + t.nh, 0);
                     }
                 };
-                if (KIND == TN && kb == nkb - 1 && t.nc % kSl != 0) {   // the clearer passes it on
+                if (KIND == TN && kb == nkb - 1 && t.nc % 16 != 0) {   // the clearer passes it on
                     if (elect_one()) {
                         mbar_arrive_expect_tx(&raw[stage], bytes);
                         loads(std::false_type{}, smem_u32(&raw[stage]));
@@ -367,7 +368,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
                     }
                     uint32_t acc = 0;
                     for (; kb < end && ok; ++kb) {
-                        if (KIND == TN && kb == nkb - 1 && t.nc % kSl != 0) {   // written by threads too, maybe the other CTA's
+                        if (KIND == TN && kb == nkb - 1 && t.nc % 16 != 0) {   // written by threads too, maybe the other CTA's
                             const uint32_t ph = (fixed_phase >> stage) & 1u;
                             ok = __all_sync(0xffffffffu, kPair ? tc::mbar_wait_cluster(&fixed[stage], ph, p.timeout_ns)
                                                                : mbar_wait(&fixed[stage], ph, p.timeout_ns));
@@ -382,9 +383,11 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
                         const uint32_t aM = smem_u32(sM + stage * kOpBytes), aN = smem_u32(sN + stage * kNBytes);
                         const uint64_t dm = kMmn ? smem_desc_mn(aM) : smem_desc_sw128(aM);
                         const uint64_t dn = kNmn ? smem_desc_mn(aN) : smem_desc_sw128(aN);
+                        const int steps = min(kSl, t.nc - kb * kSl + 15) / 16;   // 16 of the contraction each
                         if (elect_one()) {
 #pragma unroll
                             for (int k = 0; k < kSl / 16; ++k) {
+                                if (k >= steps) break;
                                 const uint64_t m = dm + (kMmn ? 128 : 2) * k, n = dn + (kNmn ? 128 : 2) * k;
                                 if (kPair) tc::tc_mma2_bf16(d_tmem, m, n, idesc, acc);
                                 else tc_mma_bf16(d_tmem, m, n, idesc, acc);
@@ -425,15 +428,16 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
                 const Tile t = tile(i);
                 const int nkb = (t.nc + kSl - 1) / kSl, left = t.nc % kSl;
                 it += nkb;
-                if (left == 0) continue;
+                if (t.nc % 16 == 0) continue;
                 const int stage = (it - 1) % kStages;
                 if (!__all_sync(0xffffffffu, mbar_wait(&raw[stage], (raw_phase >> stage) & 1u, p.timeout_ns))) break;
                 raw_phase ^= 1u << stage;
-                const int n16 = (kSl - left) * 8;   // 16-byte pieces of the cleared rows in each chunk of 64 values
-                for (int b = 0; b < 4; ++b) {
-                    uint4 *q = reinterpret_cast<uint4 *>((b < 2 ? sM : sN) + stage * kOpBytes + (b & 1) * (kOpBytes / 2)) +
-                               left * 8;
-                    for (int j = lane; j < n16; j += 32) q[j] = make_uint4(0, 0, 0, 0);
+                // up to the next 16: 16-byte pieces of the cleared rows in each chunk of 64 values
+                const int n16 = (16 - left % 16) * 8;
+                for (int j = lane; j < 4 * n16; j += 32) {
+                    const int b = j / n16;
+                    uint4 *q = reinterpret_cast<uint4 *>((b < 2 ? sM : sN) + stage * kOpBytes + (b & 1) * (kOpBytes / 2));
+                    q[left * 8 + j - b * n16] = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
