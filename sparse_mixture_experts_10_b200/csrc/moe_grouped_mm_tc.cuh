@@ -58,12 +58,13 @@ __device__ __forceinline__ int run_length(int nkb) {
     const int runs = (nkb + kRun - 1) / kRun;
     return (nkb + runs - 1) / runs;
 }
-constexpr int kMaxStages = 6;
 
-// Slices in the ring: 192 KB of shared memory either way.
-__host__ __device__ constexpr int ring_stages(bool wide) { return wide ? 4 : 6; }
+// Slices in the ring: 192 KB of shared memory, in TN with a buffer of their own for the last slices of segments.
+// Those are copied when a tile begins and used when it ends, so that clearing them stays off the critical path
+// (in the ring, 18 gradients of 4096 x 2048 took 213 us over 520 rows and 187 us over 528, which need no clearing).
+__host__ __device__ constexpr int ring_stages(int kind, bool wide) { return wide ? 4 : kind == TN ? 5 : 6; }
 __host__ __device__ constexpr size_t tc_smem_bytes(int groups) {
-    return 1024 + (size_t)12 * kOpBytes + (4 * kMaxStages + 5) * 8 + 16 + 8 * (size_t)(groups + 1);
+    return 1024 + (size_t)12 * kOpBytes + (2 * 6 + 8) * 8 + 16 + 8 * (size_t)(groups + 1);
 }
 
 // The N operand's tensor maps: K-major boxes of 16, 32, ... 128 rows, so that a slice is one copy of
@@ -229,16 +230,18 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
     constexpr bool kF32 = sizeof(TO) == 4;
     static_assert(!kWide || (kPair && KIND != TN && !kF32), "wide tiles: CTA pairs, K-major N operand, bf16 results");
     constexpr int kAccCols = kPair ? 256 : 128;
-    constexpr int kStages = ring_stages(kWide), kNBytes = (kWide ? 2 : 1) * kOpBytes;
+    constexpr int kStages = ring_stages(KIND, kWide), kNBytes = (kWide ? 2 : 1) * kOpBytes;
     constexpr bool kMmn = KIND != NT, kNmn = KIND == TN;   // MN-major operands
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = align_smem_1024(smem_raw);
     uint8_t *sM = smem, *sN = smem + kStages * kOpBytes;
-    uint64_t *full = reinterpret_cast<uint64_t *>(sN + kStages * kNBytes);
+    uint8_t *sTail = sN + kStages * kNBytes;   // TN: a segment's last slice, the M operand and then the N operand
+    uint64_t *full = reinterpret_cast<uint64_t *>(sTail + (KIND == TN ? 2 * kOpBytes : 0));
     uint64_t *empty = full + kStages;
-    uint64_t *raw = empty + kStages;   // TN: a last slice has landed and is to be cleared
-    uint64_t *fixed = raw + kStages;   // TN: ... and has been, in every CTA of the pair
-    uint64_t *tfull = fixed + kStages; // an accumulator (kWide: [0], both) is complete
+    uint64_t *raw = empty + kStages;   // TN: the last slice has landed and is to be cleared
+    uint64_t *fixed = raw + 1;         // ... has been, in every CTA of the pair
+    uint64_t *used = fixed + 1;        // ... and has been used
+    uint64_t *tfull = used + 1;        // an accumulator (kWide: [0], both) is complete
     uint64_t *tempty = tfull + 2;      // an accumulator has been read
     uint64_t *drain = tempty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
@@ -254,9 +257,10 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
-            mbar_init(&raw[s], 1);
-            mbar_init(&fixed[s], kPair ? 2 : 1);
         }
+        mbar_init(raw, 1);
+        mbar_init(fixed, kPair ? 2 : 1);
+        mbar_init(used, 1);
         for (int a = 0; a < 2; ++a) {
             mbar_init(&tfull[a], 1);
             mbar_init(&tempty[a], (kPair ? 2 : 1) * kEpi);
@@ -285,7 +289,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
         uint32_t phase = 0;
         bool ok = true;
         IssuedSlots iss, iss_raw;
-        uint32_t full_phase = 0, raw_phase = 0;   // one bit per stage: TN uses either barrier of a stage
+        uint32_t tail_phase = 0;
         for (int i = first; i < total && ok; i += step) {
             const Tile t = tile(i);
             if (KIND != TN && t.rows <= 0) continue;
@@ -295,41 +299,45 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
             const int box = kNmn ? 7 : (half + 15) / 16 - 1;   // K-major: (box + 1) * 16 rows
             const uint32_t bytes = kOpBytes + t.nsub * (box + 1) * (kOpBytes / 8);
             const CUtensorMap *mapN = &tmN.m[kNmn ? 0 : box];
-            const int nkb = (t.nc + kSl - 1) / kSl;
-            for (int kb = 0; kb < nkb; ++kb) {
+            auto loads = [&](auto pair, uint32_t bar, uint8_t *dM, uint8_t *dN, int c) {
+                constexpr bool P = decltype(pair)::value;
+                if (KIND == NT) tma_load_3d<P>(&tmM, bar, dM, c, f, t.g);
+                else load_mn<P>(&tmM, p.m_chunks, bar, dM, f, c, KIND == NN ? t.g : 0);
+                if (kNmn) {
+                    load_mn<P>(mapN, p.n_chunks, bar, dN, r, c, 0);
+                } else {
+                    tma_load_3d<P>(mapN, bar, dN, c, r, 0);
+                    if (kWide && t.nsub == 2) tma_load_3d<P>(mapN, bar, dN + kOpBytes, c, r + t.nh, 0);
+                }
+            };
+            int nkb = (t.nc + kSl - 1) / kSl;   // slices through the ring
+            const bool tail = KIND == TN && t.nc % 16 != 0;
+            if (tail) --nkb;
+            for (int kb = 0; kb <= nkb && ok; ++kb) {
+                // the last slice goes out once the ring holds this tile's first ones: the tile before is then at its own
+                // last slice, and this one is not needed before all the others
+                if (tail && kb == min(nkb, kStages)) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(used, tail_phase ^ 1, p.timeout_ns));
+                    if (!ok) break;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(raw, bytes);
+                        loads(std::false_type{}, smem_u32(raw), sTail, sTail + kOpBytes, t.c0 + nkb * kSl);
+                    }
+                    iss_raw.note(0, tail_phase);
+                    tail_phase ^= 1;
+                }
+                if (kb == nkb) break;
                 if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1, p.timeout_ns))) {
                     ok = false;
                     break;
                 }
-                const int c = t.c0 + kb * kSl;
-                uint8_t *dM = sM + stage * kOpBytes, *dN = sN + stage * kNBytes;
-                auto loads = [&](auto pair, uint32_t bar) {
-                    constexpr bool P = decltype(pair)::value;
-                    if (KIND == NT) tma_load_3d<P>(&tmM, bar, dM, c, f, t.g);
-                    else load_mn<P>(&tmM, p.m_chunks, bar, dM, f, c, KIND == NN ? t.g : 0);
-                    if (kNmn) {
-                        load_mn<P>(mapN, p.n_chunks, bar, dN, r, c, 0);
-                    } else {
-                        tma_load_3d<P>(mapN, bar, dN, c, r, 0);
-                        if (kWide && t.nsub == 2) tma_load_3d<P>(mapN, bar, dN + kOpBytes, c, r + t.nh, 0);
-                    }
-                };
-                if (KIND == TN && kb == nkb - 1 && t.nc % 16 != 0) {   // the clearer passes it on
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(&raw[stage], bytes);
-                        loads(std::false_type{}, smem_u32(&raw[stage]));
-                    }
-                    iss_raw.note(stage, (raw_phase >> stage) & 1u);
-                    raw_phase ^= 1u << stage;
-                } else {
-                    const uint32_t bar = smem_u32(&full[stage]);
-                    if (elect_one()) {
-                        if (rank == 0) mbar_arrive_expect_tx(&full[stage], (kPair ? 2 : 1) * bytes);
-                        loads(std::integral_constant<bool, kPair>{}, kPair ? tc::mapa_shared(bar, 0) : bar);
-                    }
-                    iss.note(stage, (full_phase >> stage) & 1u);
-                    full_phase ^= 1u << stage;
+                const uint32_t bar = smem_u32(&full[stage]);
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], (kPair ? 2 : 1) * bytes);
+                    loads(std::integral_constant<bool, kPair>{}, kPair ? tc::mapa_shared(bar, 0) : bar,
+                          sM + stage * kOpBytes, sN + stage * kNBytes, t.c0 + kb * kSl);
                 }
+                iss.note(stage, phase);
                 if (++stage == kStages) {
                     stage = 0;
                     phase ^= 1;
@@ -346,7 +354,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
             constexpr uint32_t kIdesc = idesc_bf16_f32(kPair ? 256 : 128, 0) | (kMmn ? 1u << 15 : 0u) |
                                         (kNmn ? 1u << 16 : 0u);
             int stage = 0;
-            uint32_t full_phase = 0, fixed_phase = 0, acc_phase = 3;   // acc_phase: parity of each accumulator's last release
+            uint32_t phase = 0, tail_phase = 0, acc_phase = 3;   // acc_phase: parity of each accumulator's last release
             int local = 0;
             bool ok = true;
             for (int i = first; i < total && ok; i += step) {
@@ -368,19 +376,18 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
                     }
                     uint32_t acc = 0;
                     for (; kb < end && ok; ++kb) {
-                        if (KIND == TN && kb == nkb - 1 && t.nc % 16 != 0) {   // written by threads too, maybe the other CTA's
-                            const uint32_t ph = (fixed_phase >> stage) & 1u;
-                            ok = __all_sync(0xffffffffu, kPair ? tc::mbar_wait_cluster(&fixed[stage], ph, p.timeout_ns)
-                                                               : mbar_wait(&fixed[stage], ph, p.timeout_ns));
-                            fixed_phase ^= 1u << stage;
+                        const bool tail = KIND == TN && kb == nkb - 1 && t.nc % 16 != 0;
+                        if (tail) {   // written by threads too, maybe the other CTA's
+                            ok = __all_sync(0xffffffffu, kPair ? tc::mbar_wait_cluster(fixed, tail_phase, p.timeout_ns)
+                                                               : mbar_wait(fixed, tail_phase, p.timeout_ns));
+                            tail_phase ^= 1;
                         } else {
-                            ok = __all_sync(0xffffffffu,
-                                            mbar_wait(&full[stage], (full_phase >> stage) & 1u, p.timeout_ns));
-                            full_phase ^= 1u << stage;
+                            ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, p.timeout_ns));
                         }
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t aM = smem_u32(sM + stage * kOpBytes), aN = smem_u32(sN + stage * kNBytes);
+                        const uint32_t aM = smem_u32(tail ? sTail : sM + stage * kOpBytes);
+                        const uint32_t aN = smem_u32(tail ? sTail + kOpBytes : sN + stage * kNBytes);
                         const uint64_t dm = kMmn ? smem_desc_mn(aM) : smem_desc_sw128(aM);
                         const uint64_t dn = kNmn ? smem_desc_mn(aN) : smem_desc_sw128(aN);
                         const int steps = min(kSl, t.nc - kb * kSl + 15) / 16;   // 16 of the contraction each
@@ -396,12 +403,16 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
                                     tc::tc_mma2_bf16(d_tmem + kAccCols, m, n + (kOpBytes >> 4), idesc, acc);
                                 acc = 1;
                             }
-                            if (kPair) tc::tc_commit2_mc(&empty[stage], 0x3);
-                            else tc_commit(&empty[stage]);
+                            uint64_t *done = tail ? used : &empty[stage];
+                            if (kPair) tc::tc_commit2_mc(done, 0x3);
+                            else tc_commit(done);
                         }
                         acc = 1;
                         __syncwarp();
-                        if (++stage == kStages) stage = 0;
+                        if (!tail && ++stage == kStages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
                     }
                     if (ok && elect_one()) {
                         if (kPair) tc::tc_commit2_mc(&tfull[a0], 0x3);
@@ -422,28 +433,23 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
     } else if (warp == kEpi + 2) {
         // ------------------------------------------------------------ TN: rows behind the segment's end
         if (KIND == TN) {
-            int it = 0;
-            uint32_t raw_phase = 0;
+            uint32_t tail_phase = 0;
             for (int i = first; i < total; i += step) {
                 const Tile t = tile(i);
-                const int nkb = (t.nc + kSl - 1) / kSl, left = t.nc % kSl;
-                it += nkb;
                 if (t.nc % 16 == 0) continue;
-                const int stage = (it - 1) % kStages;
-                if (!__all_sync(0xffffffffu, mbar_wait(&raw[stage], (raw_phase >> stage) & 1u, p.timeout_ns))) break;
-                raw_phase ^= 1u << stage;
+                if (!__all_sync(0xffffffffu, mbar_wait(raw, tail_phase, p.timeout_ns))) break;
+                tail_phase ^= 1;
                 // up to the next 16: 16-byte pieces of the cleared rows in each chunk of 64 values
-                const int n16 = (16 - left % 16) * 8;
+                const int left = t.nc % kSl, n16 = (16 - left % 16) * 8;
                 for (int j = lane; j < 4 * n16; j += 32) {
                     const int b = j / n16;
-                    uint4 *q = reinterpret_cast<uint4 *>((b < 2 ? sM : sN) + stage * kOpBytes + (b & 1) * (kOpBytes / 2));
-                    q[left * 8 + j - b * n16] = make_uint4(0, 0, 0, 0);
+                    reinterpret_cast<uint4 *>(sTail + b * (kOpBytes / 2))[left * 8 + j - b * n16] = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    if (kPair) tc::mbar_arrive_remote(tc::mapa_shared(smem_u32(&fixed[stage]), 0));
-                    else mbar_arrive(&fixed[stage]);
+                    if (kPair) tc::mbar_arrive_remote(tc::mapa_shared(smem_u32(fixed), 0));
+                    else mbar_arrive(fixed);
                 }
             }
         }
