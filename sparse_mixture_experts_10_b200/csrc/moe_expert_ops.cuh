@@ -51,7 +51,8 @@ int make_gmm_plan(const moe_gmm *d, int64_t rows, GmmPlan *out) {
     p.n = d->n;
     p.k = d->k;
     p.accumulate = d->accumulate;
-    p.timeout_ns = kTimeoutNs;
+    // a wait lasts at most one tile: about half a microsecond for 64 of the contraction, 2 allowed
+    p.timeout_ns = kTimeoutNs + 32ull * (uint64_t)std::max<int64_t>(rows, std::max(d->n, d->k));
     return MOE_OK;
 }
 
@@ -66,7 +67,7 @@ int launch_gmm_simt(gmm::Params p, const DeviceInfo &dev, cudaStream_t s) {
     } else {
         upper = (cdiv(p.rows, gmm::kTile) + std::min<int64_t>(p.G, p.rows)) * p.n_tiles;
     }
-    if (upper > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    if (upper > INT32_MAX - 65536) return MOE_ERR_UNSUPPORTED;   // tile counters step past the last one
     p.total = (int)upper;
     const unsigned grid = (unsigned)std::min<int64_t>(upper, (int64_t)dev.sms * 6);
     return launch_pdl(gmm::simt_kernel<KIND>, dim3(grid), dim3(gmm::kSimtThreads), 0, s, p);
@@ -131,7 +132,7 @@ int launch_gmm_tc(gmm::Params p, const DeviceInfo &dev, cudaStream_t s) {
     p.n_tiles = (int)cdiv(p.n, unit);
     const int64_t upper = KIND == gmm::TN ? (int64_t)p.G * p.m_tiles * p.n_tiles
                                           : (cdiv(p.rows, unit) + live) * p.m_tiles;
-    if (upper > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    if (upper > INT32_MAX - 65536) return MOE_ERR_UNSUPPORTED;   // tile counters step past the last one
     p.total = (int)upper;
     const size_t smem = gmm::tc_smem_bytes(p.G);
     if (pair) {

@@ -139,6 +139,62 @@ def test_grouped_mm_strides_and_rows_outside_the_segments(kind, dt, out):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dt,out", TYPES)
+@pytest.mark.parametrize("lengths", [[64, 16, 48, 15, 17, 31, 33], [1040, 1024, 1008], [2000]])
+def test_grouped_mm_widths_of_whole_chunks(kind, dt, out, lengths):
+    """Widths that are multiples of 64 (with row strides that are not), lengths around multiples of 16 and 64."""
+    gmm_case(kind, lengths, 320, 192, dt, out, seed=len(lengths), start=5, extra=3, pads=(24, 8, 16))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+def test_grouped_mm_long_sums_in_fp32(kind):
+    """fp32 results of bf16 operands over 16384 terms: runs of at most 768 terms, 16 a step, each step off by
+    at most 2^-23 of a partial sum, then at most 22 roundings of the runs' sum."""
+    terms, other = 16384, 264
+    g = gen(41)
+    tn = kind == moe.MOE_GMM_TN
+    n, k = (other, 136) if tn else (other, terms) if kind == moe.MOE_GMM_NT else (terms, other)
+    rows = terms if tn else 130
+    a = randn(g, rows, k if kind == moe.MOE_GMM_NT else n)
+    b = randn(g, rows, k) if tn else randn(g, 1, n, k)
+    c = torch.empty(*((1, n) if tn else (rows,)), n if kind == moe.MOE_GMM_NT else k, device="cuda")
+    d = moe.make_gmm(kind, 1, n, k, moe.MOE_BF16, moe.MOE_F32)
+    moe.check(moe.moe_grouped_mm(d, a, b, c, torch.tensor([0, rows], dtype=torch.int32, device="cuda"), rows))
+    ref, S = gmm_reference(kind, a, b, [0, rows], c.shape)
+    close(c, ref, (768 / 16 + 22) * 2.0 ** -23 * S)
+    # and in all no more than 1e-6 of the result: the losses towards zero do not add up over the whole length
+    assert relative(c, ref) <= 1e-6
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+def test_grouped_mm_graph_follows_new_offsets(kind):
+    """A captured call reads its offsets when it is replayed: any other segments of as many rows."""
+    n, k, rows = 136, 200, 400
+    g = gen(42)
+    tn = kind == moe.MOE_GMM_TN
+    a = randn(g, rows, k if kind == moe.MOE_GMM_NT else n)
+    b = randn(g, rows, k) if tn else randn(g, 4, n, k)
+    c = torch.empty(*((4, n) if tn else (rows,)), n if kind == moe.MOE_GMM_NT else k, device="cuda")
+    o = torch.tensor([0, 100, 200, 300, 400], dtype=torch.int32, device="cuda")
+    d = moe.make_gmm(kind, 4, n, k, moe.MOE_BF16, moe.MOE_F32)
+    moe.check(moe.moe_grouped_mm(d, a, b, c, o, rows))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.check(moe.moe_grouped_mm(d, a, b, c, o, rows))
+    for off in ([0, 0, 0, 0, 400], [0, 1, 399, 399, 400], [0, 257, 258, 300, 400]):
+        o.copy_(torch.tensor(off, dtype=torch.int32))
+        c.fill_(7.0)
+        graph.replay()
+        assert status_clear() == 0
+        ref, S = gmm_reference(kind, a, b, off, c.shape)
+        close(c, ref, (400 + 8) * 2.0 ** -23 * S)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_grouped_mm_many_groups(kind, dt):
     g = torch.Generator().manual_seed(3)
@@ -687,6 +743,44 @@ def test_q4_matvec_streams_and_graphs():
     for how in (in_graph, on_two_streams):
         again, _ = q4_case(*args, seed=5, run=how)
         assert torch.equal(first, again)
+
+
+@pytest.mark.gpu
+def test_q4_matvec_graph_follows_new_experts():
+    """A captured call reads its experts when it is replayed."""
+    N, n, k, pairs = 8, 96, 416, 24
+    g = gen(43)
+    codes, scales = q4_weights(g, N, n, k, 32, moe.MOE_Q4_INT4)
+    x = randn(g, pairs, k)
+    e = torch.zeros(pairs, dtype=torch.int32, device="cuda")
+    y = torch.empty(pairs, n, device="cuda")
+    d = moe.make_q4(N, n, k, 32)
+    call = lambda: moe.check(moe.moe_q4_matvec(d, x, pairs, 1, e, codes, scales, None, y, moe.MOE_F32))
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    W = q4_values(codes, scales, k, 32, moe.MOE_Q4_INT4)
+    for new in ([3] * pairs, list(range(8)) * 3, [-1] * 20 + [7, 0, 7, 1]):
+        e.copy_(torch.tensor(new, dtype=torch.int32))
+        y.fill_(9.0)
+        graph.replay()
+        assert status_clear() == 0
+        for p, ex in enumerate(new):
+            ref, S = (W[ex] @ x[p].to(F64), W[ex].abs() @ x[p].to(F64).abs()) if ex >= 0 else (torch.zeros(n, dtype=F64, device="cuda"),) * 2
+            close(y[p], ref, (k + 8) * 2.0 ** -23 * S)
+
+
+@pytest.mark.gpu
+def test_q4_matvec_wide_rows():
+    """Rows of x of which shared memory holds only a few at a time, and one at the limit; longer ones are refused."""
+    q4_case(2, 32, 14336, 128, moe.MOE_Q4_INT4, moe.MOE_ACT_NONE, 9, 1, F32, False, seed=1)
+    q4_case(2, 16, 40960, 32, moe.MOE_Q4_E2M1, moe.MOE_ACT_SWIGLU, 3, 1, F32, False, seed=2)
+    d = moe.make_q4(1, 16, 1 << 20, 128)
+    t = torch.empty(1 << 20, dtype=BF, device="cuda")
+    e = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert moe.moe_q4_matvec(d, t, 1, 1, e, t, t, None, t, moe.MOE_F32) == moe.MOE_ERR_UNSUPPORTED
 
 
 @pytest.mark.gpu
