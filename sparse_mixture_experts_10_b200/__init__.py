@@ -188,9 +188,7 @@ def load_library():
 
 # ------------------------------------------------------------------ marshalling helpers
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 

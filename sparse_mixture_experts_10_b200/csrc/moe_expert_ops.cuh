@@ -115,10 +115,10 @@ int launch_gmm_tc(gmm::Params p, const DeviceInfo &dev, cudaStream_t s) {
                              &p.m_chunks));
     if (KIND == gmm::TN) {
         MOE_TRY(make_map_mn(&mn.m[0], p.A, 1, p.rows, p.n, p.lda, &p.n_chunks));
-        for (int i = 1; i < 8; ++i) mn.m[i] = mn.m[0];
+        for (int i = 1; i < 5; ++i) mn.m[i] = mn.m[0];
     } else {
-        for (int i = 0; i < 8; ++i)
-            MOE_TRY(make_map_k(&mn.m[i], p.A, 1, p.rows, KIND == gmm::NT ? p.k : p.n, p.lda, 16 * (i + 1)));
+        for (int i = 0; i < 5; ++i)
+            MOE_TRY(make_map_k(&mn.m[i], p.A, 1, p.rows, KIND == gmm::NT ? p.k : p.n, p.lda, gmm::box_rows(i)));
     }
     const int64_t F = KIND == gmm::NT ? p.n : p.k, live = std::min<int64_t>(p.G, p.rows);
     // row tiles there are at least (segments are on the device; this is what the host knows)
@@ -257,7 +257,8 @@ int launch_q4(int format, const q4::MatvecParams &p, const DeviceInfo &dev, cuda
     q.box_tiles = std::min(4, q4::kWarps / q.ks);
     CUtensorMap map;
     MOE_TRY(make_map_codes(&map, q.codes, q.N, q.n, q.k / 2, q.act == MOE_ACT_SWIGLU, q.box_tiles));
-    const dim3 grid((unsigned)std::min<int64_t>(dev.sms, live * q.tiles));
+    const int64_t lots = live + p.pairs / q.cols_pass;   // at most
+    const dim3 grid((unsigned)std::min<int64_t>(dev.sms, lots * q.tiles));
     auto *k = format == MOE_Q4_E2M1      ? q4::matvec_kernel<q4::E2M1, 5>
               : p.group_shift == 5       ? q4::matvec_kernel<q4::INT4, 5>
               : p.group_shift == 6       ? q4::matvec_kernel<q4::INT4, 6>

@@ -84,8 +84,8 @@ struct Params {
 };
 
 // CUDA-core kernel for fp32 operands: 64 x 64 tiles, slices of 32 along the
-// contraction in two shared-memory buffers (the next slice travels in registers
-// meanwhile), two halves of 128 threads with 8 x 4 results each as pairs of rows
+// contraction in two shared-memory buffers (the next two slices travel in
+// registers meanwhile), two halves of 128 threads with 8 x 4 results each as pairs of rows
 // (one f32x2 multiply-add for two); either half takes 16 of a slice's 32 steps,
 // and their fp32 sums are added at the end.  12 floats are read from shared
 // memory for 32 multiply-adds; the second half doubles the warps that hide
@@ -129,8 +129,8 @@ __global__ void __launch_bounds__(kSimtThreads) simt_kernel(const Params p) {
             hi = KIND == NT ? p.k : p.n;
         }
         const float *Bg = KIND == TN ? B : B + (int64_t)g * p.n * p.ldb;
-        float4 a[kV], b[kV];
-        auto fetch = [&](int kk) {
+        float4 a0[kV], b0[kV], a1[kV], b1[kV];   // the next slice and the one after it, on their way
+        auto fetch = [&](int kk, float4 (&a)[kV], float4 (&b)[kV]) {
 #pragma unroll
             for (int h = 0; h < kV; ++h) {
                 const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kSimtThreads) simt_kernel(const Params p) {
                 else b[h] = kk + mr < hi && n0 + mh < cols ? at(Bg + (kk + mr) * p.ldb + n0 + mh) : z;
             }
         };
-        auto put = [&](int buf) {
+        auto put = [&](int buf, const float4 (&a)[kV], const float4 (&b)[kV]) {
 #pragma unroll
             for (int h = 0; h < kV; ++h) {
                 const int kh = kc + 4 * h, mh = mc + 4 * h;
@@ -165,31 +165,35 @@ __global__ void __launch_bounds__(kSimtThreads) simt_kernel(const Params p) {
         for (int x = 0; x < 4; ++x)
 #pragma unroll
             for (int y = 0; y < 4; ++y) acc[x][y] = 0;
-        int buf = 0;
-        if (lo < hi) {
-            fetch(lo);
-            put(0);
-        }
-        __syncthreads();
-        for (int kk = lo; kk < hi; kk += kSlice, buf ^= 1) {
-            const bool more = kk + kSlice < hi;
-            if (more) fetch(kk + kSlice);
+        auto multiply = [&](int buf) {
 #pragma unroll
             for (int q0 = 0; q0 < kSlice / 2; ++q0) {
                 const int q = half * (kSlice / 2) + q0;
-                const ulonglong2 a0 = *reinterpret_cast<const ulonglong2 *>(&As[buf][q][ty * 8]);
-                const ulonglong2 a1 = *reinterpret_cast<const ulonglong2 *>(&As[buf][q][ty * 8 + 4]);
+                const ulonglong2 av0 = *reinterpret_cast<const ulonglong2 *>(&As[buf][q][ty * 8]);
+                const ulonglong2 av1 = *reinterpret_cast<const ulonglong2 *>(&As[buf][q][ty * 8 + 4]);
                 const float4 bv = *reinterpret_cast<const float4 *>(&Bs[buf][q][tx * 4]);
-                const uint64_t ar[4] = {a0.x, a0.y, a1.x, a1.y};
+                const uint64_t ar[4] = {av0.x, av0.y, av1.x, av1.y};
                 const uint64_t br[4] = {f2_splat(bv.x), f2_splat(bv.y), f2_splat(bv.z), f2_splat(bv.w)};
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
 #pragma unroll
                     for (int y = 0; y < 4; ++y) acc[x][y] = f2_fma(ar[x], br[y], acc[x][y]);
             }
-            if (more) put(buf ^ 1);
+        };
+        if (lo < hi) fetch(lo, a0, b0);
+        if (lo + kSlice < hi) fetch(lo + kSlice, a1, b1);
+        for (int kk = lo; kk < hi; kk += 2 * kSlice) {   // two slices a turn, one per buffer and register set
+            put(0, a0, b0);
+            if (kk + 2 * kSlice < hi) fetch(kk + 2 * kSlice, a0, b0);
             __syncthreads();
+            multiply(0);
+            if (kk + kSlice >= hi) break;
+            put(1, a1, b1);
+            if (kk + 3 * kSlice < hi) fetch(kk + 3 * kSlice, a1, b1);
+            __syncthreads();
+            multiply(1);
         }
+        __syncthreads();
         // the second half's sums, through the operands' buffers
         uint64_t *s_sum = reinterpret_cast<uint64_t *>(&s_ab[0][0][0][0]) + (tid & 127);
         if (half) {

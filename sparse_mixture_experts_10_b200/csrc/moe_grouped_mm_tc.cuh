@@ -67,12 +67,13 @@ __host__ __device__ constexpr size_t tc_smem_bytes(int groups) {
     return 1024 + (size_t)12 * kOpBytes + (2 * 6 + 8) * 8 + 16 + 8 * (size_t)(groups + 1);
 }
 
-// The N operand's tensor maps: K-major boxes of 16, 32, ... 128 rows, so that a slice is one copy of
-// just the tile's rows (192-row tiles in copies of 32 rows ran at 930 TFLOP/s, in one of 96 at 1166); TN uses
+// The N operand's tensor maps: K-major boxes of 16, 32, 64, 96 and 128 rows, so that a slice is one copy
+// of nearly the tile's rows (192-row tiles in copies of 32 rows ran at 930 TFLOP/s, in one of 96 at 1166); TN uses
 // the first.
 struct NMaps {
-    CUtensorMap m[8];
+    CUtensorMap m[5];
 };
+constexpr int box_rows(int i) { return i == 0 ? 16 : 32 * i; }
 
 // cp.async.bulk.tensor of a 3-D box; kPair: completion on the leader CTA's barrier.
 template <bool kPair>
@@ -269,7 +270,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
         fence_mbar_init();
         tma_prefetch_desc(&tmM);
         tma_prefetch_desc(&tmN.m[0]);
-        if (!kNmn) tma_prefetch_desc(&tmN.m[7]);
+        if (!kNmn) tma_prefetch_desc(&tmN.m[4]);
     }
     if (warp == kEpi + 1) {
         if (kPair) tc::tmem_alloc2(tmem_slot, 2 * kAccCols);
@@ -296,8 +297,8 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
             const int f = t.f0 + (int)rank * 128;
             const int half = kPair ? t.nh / 2 : t.nh;   // N rows of an instruction that this CTA loads
             const int r = t.r0 + (int)rank * half;
-            const int box = kNmn ? 7 : (half + 15) / 16 - 1;   // K-major: (box + 1) * 16 rows
-            const uint32_t bytes = kOpBytes + t.nsub * (box + 1) * (kOpBytes / 8);
+            const int box = half <= 16 ? 0 : (half + 31) / 32;
+            const uint32_t bytes = kOpBytes + (kNmn ? kOpBytes : t.nsub * (box == 0 ? 16 : box * 32) * (kSl * 2));
             const CUtensorMap *mapN = &tmN.m[kNmn ? 0 : box];
             auto loads = [&](auto pair, uint32_t bar, uint8_t *dM, uint8_t *dN, int c) {
                 constexpr bool P = decltype(pair)::value;

@@ -361,7 +361,8 @@ __global__ void __launch_bounds__(kThreadsMv, 1)
     __shared__ uint64_t s_full[kMaxSlots], s_empty[kMaxSlots];
     __shared__ int s_count[kMaxExperts];             // pairs of each expert
     __shared__ uint16_t s_experts[kMaxExperts];      // the experts that have a pair, ascending
-    __shared__ int64_t s_cost0[kMaxExperts + 1];     // cost before each of them
+    __shared__ int s_cost0[kMaxExperts + 1];         // cost before each of them: all lots (at most 5120) times tiles
+                                                     // (at most 65536) times 5 stay below 2^31
     __shared__ int s_live, s_bad;
     __shared__ float s_part[kWarps][8][32];
     uint8_t *s_x = smem + p.slots * kSlotBytes;
@@ -389,24 +390,25 @@ __global__ void __launch_bounds__(kThreadsMv, 1)
         s_expert[i] = good ? (int16_t)e : (int16_t)-1;
     }
     __syncthreads();
-    // lots of pairs that are staged together, and what a tile costs with them (a lot of more than 8 pairs: 5/4)
-    auto lots = [&](int e) { return (s_count[e] + p.cols_pass - 1) / p.cols_pass; };
-    auto tile_cost = [&](int e) {
-        const int full = s_count[e] / p.cols_pass, rest = s_count[e] % p.cols_pass;
-        return full * (p.cols_pass > 8 ? 5 : 4) + (rest > 8 ? 5 : rest > 0 ? 4 : 0);
+    // An expert's pairs are staged in lots of cols_pass; its work is its tiles with the first lot, with the second and
+    // so on.  A tile costs 4, with more than 8 pairs 5 (cost_of(e, u): that of the first u of its lots * tiles).
+    auto cost_of = [&](int e, int u) {
+        const int full = s_count[e] / p.cols_pass, rest = s_count[e] - full * p.cols_pass, f = min(u, full * p.tiles);
+        return f * (p.cols_pass > 8 ? 5 : 4) + (u - f) * (rest > 8 ? 5 : 4);
     };
+    auto lots = [&](int e) { return (s_count[e] + p.cols_pass - 1) / p.cols_pass; };
     if (warp == 0) {
         int live = 0;
-        int64_t cost = 0;
+        int cost = 0;
         for (int e0 = 0; e0 < p.N; e0 += 32) {
             const int e = e0 + lane;
             const bool has = e < p.N && s_count[e] > 0;
             const uint32_t m = __ballot_sync(0xffffffffu, has);
             if (m == 0) continue;
-            int64_t c = has ? (int64_t)tile_cost(e) * p.tiles : 0, incl = c;
+            int c = has ? cost_of(e, lots(e) * p.tiles) : 0, incl = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+                const int u = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += u;
             }
             if (has) {
@@ -424,17 +426,21 @@ __global__ void __launch_bounds__(kThreadsMv, 1)
     }
     __syncthreads();
     const int live = s_live;
-    // this block's share: the tiles whose cost starts in [x0, x1)
-    const int64_t x0 = s_cost0[live] * blockIdx.x / gridDim.x, x1 = s_cost0[live] * (blockIdx.x + 1) / gridDim.x;
+    // this block's share: the work that starts in [x0, x1) of the cost
+    const int even = s_cost0[live] / (int)gridDim.x, rest_all = s_cost0[live] - even * (int)gridDim.x;
+    auto share_at = [&](int b) { return even * b + rest_all * b / (int)gridDim.x; };
+    const int x0 = share_at(blockIdx.x), x1 = share_at(blockIdx.x + 1);
     int first = 0;
     for (int hi = live - 1; first < hi;) {   // the last expert that starts at or before x0
         const int mid = (first + hi + 1) >> 1;
         if (s_cost0[mid] <= x0) first = mid;
         else hi = mid - 1;
     }
-    auto tile_at = [&](int y, int64_t x) {   // tiles of the y-th live expert that start before x
-        const int64_t c = s_cost0[y + 1] - s_cost0[y], per = c / p.tiles, d = x - s_cost0[y];
-        return d <= 0 ? 0 : (int)min((int64_t)p.tiles, (d + per - 1) / per);
+    auto work_at = [&](int y, int x) {   // how much of the y-th live expert's work starts before x
+        const int e = s_experts[y];
+        const int full = s_count[e] / p.cols_pass, rest = s_count[e] - full * p.cols_pass, f = full * p.tiles;
+        const int d = min(x, s_cost0[y + 1]) - s_cost0[y], wf = p.cols_pass > 8 ? 5 : 4, wr = rest > 8 ? 5 : 4;
+        return d <= 0 ? 0 : d <= f * wf ? (d + wf - 1) / wf : f + (d - f * wf + wr - 1) / wr;
     };
     const int step = kWarps / p.ks, chunks = (p.k + kChunk - 1) / kChunk, rounds = (chunks + p.ks - 1) / p.ks;
     if (warp == kWarps) {
@@ -446,8 +452,11 @@ __global__ void __launch_bounds__(kThreadsMv, 1)
             bool ok = true;
             IssuedSlots iss;
             for (int y = first; y < live && s_cost0[y] < x1 && ok; ++y) {
-                const int e = s_experts[y], tile0 = tile_at(y, x0), tile1 = tile_at(y, x1);
-                for (int lot = lots(e); lot > 0 && ok; --lot)
+                const int e = s_experts[y];
+                const int w1 = work_at(y, x1);
+                for (int w = work_at(y, x0); w < w1 && ok;) {   // one lot at a time
+                    const int tile0 = w % p.tiles, tile1 = min(p.tiles, tile0 + w1 - w);
+                    w += tile1 - tile0;
                     for (int tile = tile0; tile < tile1 && ok; tile += step)
                         for (int j = 0; j < rounds; ++j) {
                             if (!mbar_wait(&s_empty[slot], phase ^ 1, p.timeout_ns)) {
@@ -468,6 +477,7 @@ __global__ void __launch_bounds__(kThreadsMv, 1)
                                 phase ^= 1;
                             }
                         }
+                }
             }
             iss.drain(s_full, p.timeout_ns);   // every copy has landed before the block leaves
         }
@@ -492,8 +502,10 @@ __global__ void __launch_bounds__(kThreadsMv, 1)
     ring.full = s_full;
     ring.empty = s_empty;
     for (int y = first; y < live && s_cost0[y] < x1; ++y) {
-        const int e = s_experts[y], tile0 = tile_at(y, x0), tile1 = tile_at(y, x1);
-        if (tile0 >= tile1) continue;
+        const int e = s_experts[y];
+        const int w1 = work_at(y, x1);
+        int w = work_at(y, x0);
+        if (w >= w1) continue;
         if (y > first) group_sync(kAll, kWarps * 32);   // the last expert's list has been used
         if (warp == 0) {
             int cnt = 0;
@@ -504,9 +516,10 @@ __global__ void __launch_bounds__(kThreadsMv, 1)
                 cnt += __popc(m);
             }
         }
-        // as many pairs at a time as are staged; the weights are read again (from L2) for each lot
-        for (int c = 0; c < s_count[e]; c += p.cols_pass) {
-            const int cnt = min(s_count[e] - c, p.cols_pass);
+        while (w < w1) {   // one lot at a time; another lot reads the weights again (from L2)
+            const int lot = w / p.tiles, c = lot * p.cols_pass, cnt = min(s_count[e] - c, p.cols_pass);
+            const int tile0 = w - lot * p.tiles, tile1 = min(p.tiles, tile0 + w1 - w);
+            w += tile1 - tile0;
             group_sync(kAll, kWarps * 32);   // the list is there; the rows of x before have been used
             // x as 16-byte pieces (8 values of a lane), each as the pairs (0, 4), (1, 5), (2, 6), (3, 7); zeros from k
             // to the end of the last slice
