@@ -11,9 +11,13 @@
 // 2^(e-6)) for e4m3.  A group with an infinity or a NaN has s = 255 and reads
 // back as NaN everywhere, so a bad step stays visible.
 //
-// Bound by HBM: a few dozen instructions per value beside 8 to 12 bytes.  One
-// warp takes 16 bytes per lane of one row at a time; the group's maximum is a
-// shuffle tree over the 4 to 32 lanes that hold it.
+// Bound by HBM: a few dozen instructions per value beside 8 to 12 bytes.  A
+// lane takes four 16-byte pieces of each operand of a row at a time (one: 227
+// and 270 us, two: 210 and 261 us, four: 208 and 251 us forward and backward
+// for 65536 rows of 2 x 2048 bf16, that is 5.2 and 5.4 TB/s); the group's
+// maximum is a shuffle tree over the 4 to 32 lanes that hold it.  GELU and e4m3 in
+// 12289 rows of 2200: 35 and 45 us, 3.8 and 4.2 TB/s (the activation's
+// instructions).
 #pragma once
 
 #include <cuda_fp8.h>

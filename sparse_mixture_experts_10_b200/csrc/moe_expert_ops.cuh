@@ -121,10 +121,13 @@ int launch_gmm_tc(gmm::Params p, const DeviceInfo &dev, cudaStream_t s) {
             MOE_TRY(make_map_k(&mn.m[i], p.A, 1, p.rows, KIND == gmm::NT ? p.k : p.n, p.lda, gmm::box_rows(i)));
     }
     const int64_t F = KIND == gmm::NT ? p.n : p.k, live = std::min<int64_t>(p.G, p.rows);
-    // row tiles there are at least (segments are on the device; this is what the host knows)
+    // Tile shapes, by what the host knows (segments are on the device): the row tiles there are at least.
+    //  pairs (256 x 256) where they fill the machine: 32 x 4096 x 7168 over 512 rows each 714 us, single CTAs (128 x 128)
+    //    963 us; 6 x 1536 x 768 over 34 rows 9.7 us, single CTAs 7.5 us (twice as many SMs read);
+    //  wide pairs (256 x 512) where segments have more than 256 rows: 675 us against 714 us; 300 rows 482 against 556
     auto row_tiles = [&](int64_t unit) { return std::max(live, cdiv(p.rows, unit)); };
     const bool pair = (KIND == gmm::TN ? p.G * cdiv(p.n, 256) : row_tiles(256)) * cdiv(F, 256) >= dev.pair_clusters;
-    // tiles of up to 512 rows need both accumulators, and no registers hold an fp32 result's running sums of them
+    // (they need both accumulators, and registers cannot hold an fp32 result's running sums of 512 rows)
     const bool wide = pair && KIND != gmm::TN && sizeof(TO) == 2 && p.rows > 256 * live &&
                       row_tiles(512) * cdiv(F, 256) >= dev.pair_clusters;
     const int unit = pair ? 256 : 128;

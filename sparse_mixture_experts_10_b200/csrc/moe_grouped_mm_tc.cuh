@@ -13,9 +13,9 @@
 // multiple of 16 rows, and no tensor time goes into padding (with the rows on
 // the 256-row side a segment of 520 rows would pay for 768).
 //
-// One persistent CTA (kPair false: tiles of 128 x <=128) or CTA pair (tiles of
-// 256 x <=256, each CTA of the pair loads its 128 f's and half of the rows)
-// per SM:
+// One persistent CTA per SM (kPair false: tiles of 128 x <=128), or a CTA pair
+// per two (tiles of 256 x <=256, kWide <=512; each CTA of the pair loads its
+// 128 f's and half of the rows):
 //   epilogue   16 warps: tcgen05.ld; a lane holds one f,
 //              so a warp writes 32 consecutive values of a row (bf16: two
 //              rows of pairs after a lane exchange)
@@ -27,6 +27,13 @@
 //              may hold anything, NaN included, so both operands are cleared
 // Slices past the end of n or k are zero-filled by TMA: the weights' tensor map
 // has the group as its own dimension.
+//
+// What bounds it: large tiles, what L2 delivers to the SMs (about 61 to 74 GB/s
+// to each, whatever the tile's shape; a slice of a 256 x 512 tile is 48 KB a CTA
+// for 17 MFLOP, of a 256 x 256 one 32 KB for 8) beside the power cap; few rows, HBM.
+// 32 experts of 512 rows each, n 4096, k 7168: 675 us, 1425 TFLOP/s with 256 x 512
+// tiles, 714 us with 256 x 256, 963 us with single CTAs.  Weight gradients over
+// 512 rows (18 of 4096 x 2048, fp32): 171 us, 3.5 TB/s written.
 //
 // Every wait is bounded; on expiry the waiting role stops issuing work, the
 // status word records MOE_STATUS_TIMEOUT and the CTA drains and returns.
@@ -64,7 +71,7 @@ __device__ __forceinline__ int run_length(int nkb) {
 // (in the ring, 18 gradients of 4096 x 2048 took 213 us over 520 rows and 187 us over 528, which need no clearing).
 __host__ __device__ constexpr int ring_stages(int kind, bool wide) { return wide ? 4 : kind == TN ? 5 : 6; }
 __host__ __device__ constexpr size_t tc_smem_bytes(int groups) {
-    return 1024 + (size_t)12 * kOpBytes + (2 * 6 + 8) * 8 + 16 + 8 * (size_t)(groups + 1);
+    return 1024 + (size_t)12 * kOpBytes + (2 * 6 + 8) * 8 + 16 + 12 * (size_t)(groups + 1);
 }
 
 // The N operand's tensor maps: K-major boxes of 16, 32, 64, 96 and 128 rows, so that a slice is one copy
@@ -157,15 +164,55 @@ struct Tile {
     int c0, nc;                 // contraction start and length
 };
 
+// The order in which groups are worked on: those whose tiles take longest first, so that the blocks' last tiles are
+// short ones (32 experts of 512 +- 22 rows, n 4096, k 7168: 945 us in the groups' own order, 896 us so).  ord[j] is the j-th
+// group, cum its first tile.  By every thread of the block; s_off is complete.  Beyond kOrdered groups the tiles
+// are many and small, and the groups keep their order.
+constexpr int kOrdered = 128;
+template <int KIND>
+__device__ __forceinline__ void order_groups(const int *s_off, int G, int unit, int *cum, int *ord) {
+    auto rows = [&](int g) { return s_off[g + 1] - s_off[g]; };
+    auto tiles = [&](int g) { return (rows(g) + unit - 1) / unit; };
+    auto weight = [&](int g) { return KIND == TN ? rows(g) : rows(g) == 0 ? 0 : (rows(g) + tiles(g) - 1) / tiles(g); };
+    for (int g = threadIdx.x; g < G; g += kTcThreads) {
+        int at = g;
+        if (G <= kOrdered) {
+            const int w = weight(g);
+            at = 0;
+            for (int h = 0; h < G; ++h) {
+                const int v = weight(h);
+                at += v > w || (v == w && h < g) ? 1 : 0;
+            }
+        }
+        ord[at] = g;
+    }
+    __syncthreads();
+    if (KIND != TN && threadIdx.x < 32) {
+        int carry = 0;
+        for (int j0 = 0; j0 <= G; j0 += 32) {
+            const int j = j0 + threadIdx.x, t = j < G ? tiles(ord[j]) : 0;
+            int incl = t;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, incl, o);
+                if ((int)threadIdx.x >= o) incl += u;
+            }
+            if (j <= G) cum[j] = carry + incl - t;
+            carry += __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+    __syncthreads();
+}
+
 template <int KIND, bool kPair, bool kWide>
-__device__ __forceinline__ Tile tile_at(const Params &p, const int *s_off, const int *s_cum, int i) {
+__device__ __forceinline__ Tile tile_at(const Params &p, const int *s_off, const int *s_cum, const int *s_ord, int i) {
     constexpr int kM = kPair ? 256 : 128, kN = kPair ? 256 : 128;
     Tile t;
     t.nsub = 1;
     if (KIND == TN) {
         const int per = p.m_tiles * p.n_tiles;
-        t.g = i / per;
-        const int r = i - t.g * per;
+        const int j = i / per, r = i - j * per;
+        t.g = kPair ? s_ord[j] : j;
         t.f0 = r / p.n_tiles * kM;
         t.r0 = (r % p.n_tiles) * kN;
         t.rows = min(kN, p.n - t.r0);
@@ -181,15 +228,15 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const int *s_off, const
             if ((int64_t)s_cum[mid] * p.m_tiles <= i) lo = mid;
             else hi = mid - 1;
         }
-        t.g = lo;
+        t.g = kPair ? s_ord[lo] : lo;
         const int tiles = s_cum[lo + 1] - s_cum[lo];
         const int r = i - s_cum[lo] * p.m_tiles;
         t.f0 = r / tiles * kM;
-        const int len = s_off[lo + 1] - s_off[lo], size = (len + tiles - 1) / tiles;
+        const int len = s_off[t.g + 1] - s_off[t.g], size = (len + tiles - 1) / tiles;
         if (kWide && size > kN) t.nsub = 2;
         t.nh = ((size + t.nsub - 1) / t.nsub + 15) & ~15;
         const int at = r % tiles * t.nh * t.nsub;
-        t.r0 = s_off[lo] + at;
+        t.r0 = s_off[t.g] + at;
         t.rows = min(t.nh * t.nsub, len - at);   // not positive for a last tile that the rounding left empty
         t.c0 = 0;
         t.nc = KIND == NT ? p.k : p.n;
@@ -248,6 +295,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     int *s_off = reinterpret_cast<int *>(tmem_slot + 4);
     int *s_cum = s_off + p.G + 1;
+    int *s_ord = s_cum + p.G + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = kPair ? tc::cluster_ctarank() : 0;
     const int first = kPair ? (int)tc::cluster_id_x() : (int)blockIdx.x;
@@ -276,13 +324,17 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
         if (kPair) tc::tmem_alloc2(tmem_slot, 2 * kAccCols);
         else tmem_alloc(tmem_slot, 2 * kAccCols);
     }
+    if (kPair) {   // a single-CTA launch has about one tile per CTA, and 1 us more for this would show
+        __syncthreads();
+        order_groups<KIND>(s_off, p.G, (kWide ? 2 : 1) * kAccCols, s_cum, s_ord);
+    }
     tc_fence_before();
     __syncthreads();
     if (kPair) tc::cluster_sync();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const int total = KIND == TN ? p.total : s_cum[p.G] * p.m_tiles;
-    auto tile = [&](int i) { return tile_at<KIND, kPair, kWide>(p, s_off, s_cum, i); };
+    auto tile = [&](int i) { return tile_at<KIND, kPair, kWide>(p, s_off, s_cum, s_ord, i); };
 
     if (warp == kEpi) {
         // ------------------------------------------------------------ TMA producer
