@@ -77,7 +77,7 @@ __device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
 // that one mask each extracts; the expert's rows of x are staged in shared
 // memory in that order.
 //
-// Measured (32 experts, 5760 x 2880, int4): 64 tokens, top 4, groups of 32: 116 us,
+// Measured (32 experts, 5760 x 2880, int4): 64 tokens, top 4, groups of 32: 114 us,
 // 2.6 TB/s of a floor of 46 us at the copy rate; the data in L2 already is no
 // faster, it is the 60 instructions for each 16 rows of a group, issued at
 // 2.4 a cycle.  One token: 18 us for 5.5 us of bytes, half of it start-up (the
@@ -114,11 +114,11 @@ __device__ __forceinline__ void decode8(uint32_t w, uint32_t (&v)[4]) {
             asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(v[i]) : "r"(0x43084308u));
         }
     } else {
-        // exponent and mantissa bits at bf16's place read as value 2^-126 (subnormals included); times 2^126 exactly
-        const uint32_t e[4] = {w << 6, w << 2, w >> 2, w >> 6}, s[4] = {w << 12, w << 8, w << 4, w};
+        // one multiplication puts the sign at bit 15 (2^12) and the other three bits at bf16's lowest exponent bits and
+        // highest mantissa bit (2^6); what they read as is value 2^-126, subnormals included: times 2^126 exactly
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[i] = and_or(e[i], 0x01c001c0u, s[i] & 0x80008000u);
+            v[i] = ((w >> (4 * i)) & 0x000f000fu) * 0x1040u & 0x81c081c0u;
             asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v[i]) : "r"(0x7e807e80u));
         }
     }
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreadsMv, 1)
     __shared__ int s_count[kMaxExperts];             // pairs of each expert
     __shared__ uint16_t s_experts[kMaxExperts];      // the experts that have a pair, ascending
     __shared__ int s_cost0[kMaxExperts + 1];         // cost before each of them: all lots (at most 5120) times tiles
-                                                     // (at most 65536) times 5 stay below 2^31
+                                                     // (at most 65536) times 4 stay below 2^31
     __shared__ int s_live, s_bad;
     __shared__ float s_part[kWarps][8][32];
     uint8_t *s_x = smem + p.slots * kSlotBytes;
@@ -384,10 +384,12 @@ __global__ void __launch_bounds__(kThreadsMv, 1)
     }
     __syncthreads();
     // An expert's pairs are staged in lots of cols_pass; its work is its tiles with the first lot, with the second and
-    // so on.  A tile costs 4, with more than 8 pairs 5 (cost_of(e, u): that of the first u of its lots * tiles).
+    // so on.  A tile costs 3, with more than 8 pairs 4 (8 experts with 8 pairs each 49 us, with 16 each 70 us; a
+    // batch of 64 tokens over 32 experts took 132 us with all tiles alike, 124 us so).  cost_of(e, u): that of the first u
+    // of an expert's lots * tiles.
     auto cost_of = [&](int e, int u) {
         const int full = s_count[e] / p.cols_pass, rest = s_count[e] - full * p.cols_pass, f = min(u, full * p.tiles);
-        return f * (p.cols_pass > 8 ? 5 : 4) + (u - f) * (rest > 8 ? 5 : 4);
+        return f * (p.cols_pass > 8 ? 4 : 3) + (u - f) * (rest > 8 ? 4 : 3);
     };
     auto lots = [&](int e) { return (s_count[e] + p.cols_pass - 1) / p.cols_pass; };
     if (warp == 0) {
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__(kThreadsMv, 1)
     auto work_at = [&](int y, int x) {   // how much of the y-th live expert's work starts before x
         const int e = s_experts[y];
         const int full = s_count[e] / p.cols_pass, rest = s_count[e] - full * p.cols_pass, f = full * p.tiles;
-        const int d = min(x, s_cost0[y + 1]) - s_cost0[y], wf = p.cols_pass > 8 ? 5 : 4, wr = rest > 8 ? 5 : 4;
+        const int d = min(x, s_cost0[y + 1]) - s_cost0[y], wf = p.cols_pass > 8 ? 4 : 3, wr = rest > 8 ? 4 : 3;
         return d <= 0 ? 0 : d <= f * wf ? (d + wf - 1) / wf : f + (d - f * wf + wr - 1) / wr;
     };
     const int step = kWarps / p.ks, chunks = (p.k + kChunk - 1) / kChunk, rounds = (chunks + p.ks - 1) / p.ks;
