@@ -172,29 +172,54 @@ int make_ckpt_params(const moe_ckpt *d, int64_t rows, ckpt::Params *p) {
     p->width = d->width;
     p->group_shift = d->group == 32 ? 5 : d->group == 64 ? 6 : 7;
     p->sgroups = (int)cdiv(d->width, d->group);
-    // warps of a block that share a row: as many as the row has pieces for (512 bytes a load, kUnroll loads at a time)
-    const int64_t pieces = cdiv((int64_t)d->width * es, 512 * ckpt::kUnroll);
+    return MOE_OK;
+}
+
+// Sets the warps of a block that share a row: as many as the row has pieces for (512 bytes a load, `unroll` loads at
+// a time).
+void set_row_warps(ckpt::Params *p, int64_t es, int unroll) {
+    const int64_t pieces = cdiv((int64_t)p->width * es, 512 * unroll);
     p->row_warps = 1;
     while (p->row_warps < ckpt::kThreads / 32 && p->row_warps * 2 <= pieces) p->row_warps *= 2;
-    return MOE_OK;
+}
+
+// One load at a time where all warps of the machine (64 an SM) have at most one piece each.
+int ckpt_unroll(const ckpt::Params &p, int64_t es, const DeviceInfo &dev) {
+    return p.rows * cdiv((int64_t)p.width * es, 512) <= (int64_t)dev.sms * 64 ? 1 : ckpt::kManyUnroll;
 }
 
 dim3 ckpt_grid(const ckpt::Params &p) {
     return dim3((unsigned)cdiv(p.rows, (ckpt::kThreads / 32) / p.row_warps));
 }
 
+template <typename T, int FMT, int U>
+int launch_ckpt_forward_u(int act, ckpt::Params p, cudaStream_t s) {
+    set_row_warps(&p, sizeof(T), U);
+    auto *k = act == MOE_ACT_GELU     ? ckpt::forward_kernel<T, ckpt::GELU, FMT, U>
+              : act == MOE_ACT_SWIGLU ? ckpt::forward_kernel<T, ckpt::SWIGLU, FMT, U>
+                                      : ckpt::forward_kernel<T, ckpt::NONE, FMT, U>;
+    return launch_pdl(k, ckpt_grid(p), dim3(ckpt::kThreads), 0, s, p);
+}
 template <typename T, int FMT>
 int launch_ckpt_forward(int act, const ckpt::Params &p, cudaStream_t s) {
-    auto *k = act == MOE_ACT_GELU     ? ckpt::forward_kernel<T, ckpt::GELU, FMT>
-              : act == MOE_ACT_SWIGLU ? ckpt::forward_kernel<T, ckpt::SWIGLU, FMT>
-                                      : ckpt::forward_kernel<T, ckpt::NONE, FMT>;
+    DeviceInfo *dev = nullptr;
+    MOE_TRY(device_info(&dev));
+    return ckpt_unroll(p, sizeof(T), *dev) == 1 ? launch_ckpt_forward_u<T, FMT, 1>(act, p, s)
+                                                : launch_ckpt_forward_u<T, FMT, ckpt::kManyUnroll>(act, p, s);
+}
+template <typename T, int FMT, int U>
+int launch_ckpt_backward_u(int act, ckpt::Params p, cudaStream_t s) {
+    set_row_warps(&p, sizeof(T), U);
+    auto *k = act == MOE_ACT_GELU ? ckpt::backward_kernel<T, ckpt::GELU, FMT, U>
+                                  : ckpt::backward_kernel<T, ckpt::SWIGLU, FMT, U>;
     return launch_pdl(k, ckpt_grid(p), dim3(ckpt::kThreads), 0, s, p);
 }
 template <typename T, int FMT>
 int launch_ckpt_backward(int act, const ckpt::Params &p, cudaStream_t s) {
-    auto *k = act == MOE_ACT_GELU ? ckpt::backward_kernel<T, ckpt::GELU, FMT>
-                                  : ckpt::backward_kernel<T, ckpt::SWIGLU, FMT>;
-    return launch_pdl(k, ckpt_grid(p), dim3(ckpt::kThreads), 0, s, p);
+    DeviceInfo *dev = nullptr;
+    MOE_TRY(device_info(&dev));
+    return ckpt_unroll(p, sizeof(T), *dev) == 1 ? launch_ckpt_backward_u<T, FMT, 1>(act, p, s)
+                                                : launch_ckpt_backward_u<T, FMT, ckpt::kManyUnroll>(act, p, s);
 }
 
 // ---------------------------------------------------------------- 4-bit weights
@@ -352,6 +377,7 @@ int moe_ckpt_load(const moe_ckpt *d, const uint8_t *q, const uint8_t *scales, in
     p.ldh = p.ldu;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int halves = d->act == MOE_ACT_SWIGLU ? 2 : 1;
+    set_row_warps(&p, elem_size(d->dtype), 1);
     auto *k = d->dtype == MOE_F32
                   ? (d->format == MOE_CKPT_INT8 ? ckpt::load_kernel<float, ckpt::INT8>
                                                 : ckpt::load_kernel<float, ckpt::E4M3>)

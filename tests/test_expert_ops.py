@@ -397,7 +397,8 @@ FORMATS = [moe.MOE_CKPT_INT8, moe.MOE_CKPT_E4M3]
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("rows,width,group", [(1, 8, 32), (3, 72, 32), (5, 264, 64), (2, 2200, 128), (9, 256, 128),
-                                              (7, 4104, 64), (130, 520, 32)])
+                                              (7, 4104, 64), (130, 520, 32), (5200, 328, 64),
+                                              (2400, 2056, 128)])
 def test_ckpt_forward_and_backward(act, dt, fmt, rows, width, group):
     halves = 2 if act == "swiglu" else 1
     u = ckpt_inputs(rows, halves * width, dt, rows + width)
