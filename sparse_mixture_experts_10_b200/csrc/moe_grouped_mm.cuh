@@ -182,18 +182,19 @@ __global__ void __launch_bounds__(kSimtThreads) simt_kernel(const Params p) {
                     for (int y = 0; y < 4; ++y) acc[x][y] = f2_fma(ar[x], br[y], acc[x][y]);
             }
         };
+        const bool active = m0 + ((tid & 127) >> 5) * 16 < m_hi;   // a warp whose 16 rows are past the segment's end rests
         if (lo < hi) fetch(lo, a0, b0);
         if (lo + kSlice < hi) fetch(lo + kSlice, a1, b1);
         for (int kk = lo; kk < hi; kk += 2 * kSlice) {   // two slices a turn, one per buffer and register set
             put(0, a0, b0);
             if (kk + 2 * kSlice < hi) fetch(kk + 2 * kSlice, a0, b0);
             __syncthreads();
-            multiply(0);
+            if (active) multiply(0);
             if (kk + kSlice >= hi) break;
             put(1, a1, b1);
             if (kk + 3 * kSlice < hi) fetch(kk + 3 * kSlice, a1, b1);
             __syncthreads();
-            multiply(1);
+            if (active) multiply(1);
         }
         __syncthreads();
         // the second half's sums, through the operands' buffers
