@@ -89,9 +89,9 @@ struct Params {
 // (one f32x2 multiply-add for two); either half takes 16 of a slice's 32 steps,
 // and their fp32 sums are added at the end.  12 floats are read from shared
 // memory for 32 multiply-adds; the second half doubles the warps that hide
-// the latencies where there are few tiles.  8 x 1024 x 256 over 1024 rows: 27 us;
-// 4 x 1536 x 1536 over 2048 rows: 282 (NT), 263 (NN), 237 us (TN), up to 41 TFLOP/s of
-// about 70; what is left is latency between slices (four warps a scheduler).
+// the latencies where there are few tiles.  8 x 1024 x 256 over 1024 rows: 23 us;
+// 4 x 1536 x 1536 over 2048 rows: 249 (NT), 242 (NN), 243 us (TN), 40 TFLOP/s of about
+// 70; what is left is latency between slices (four warps a scheduler).
 constexpr int kTile = 64, kSlice = 32, kSimtThreads = 256;
 
 template <int KIND>
@@ -144,21 +144,26 @@ __global__ void __launch_bounds__(kSimtThreads) simt_kernel(const Params p) {
                 else b[h] = kk + mr < hi && n0 + mh < cols ? at(Bg + (kk + mr) * p.ldb + n0 + mh) : z;
             }
         };
+        // Step k of a slice has its columns rotated by 8 (k / 8): a K-major operand is stored transposed, by lanes that hold
+        // the steps 0, 8, 16 and 24 of 8 rows, and they then meet 32 different banks instead of 8 (283 -> 249 us).
+        auto col = [](int k, int m) { return (m + (k & ~7)) & (kTile - 1); };
         auto put = [&](int buf, const float4 (&a)[kV], const float4 (&b)[kV]) {
 #pragma unroll
             for (int h = 0; h < kV; ++h) {
                 const int kh = kc + 4 * h, mh = mc + 4 * h;
                 if (KIND == TN) {
-                    *reinterpret_cast<float4 *>(&As[buf][mr][mh]) = a[h];
+                    *reinterpret_cast<float4 *>(&As[buf][mr][col(mr, mh)]) = a[h];
                 } else {
-                    As[buf][kh][kr] = a[h].x; As[buf][kh + 1][kr] = a[h].y;
-                    As[buf][kh + 2][kr] = a[h].z; As[buf][kh + 3][kr] = a[h].w;
+                    const int c = col(kh, kr);   // kh .. kh + 3 are in one group of 8
+                    As[buf][kh][c] = a[h].x; As[buf][kh + 1][c] = a[h].y;
+                    As[buf][kh + 2][c] = a[h].z; As[buf][kh + 3][c] = a[h].w;
                 }
                 if (KIND == NT) {
-                    Bs[buf][kh][kr] = b[h].x; Bs[buf][kh + 1][kr] = b[h].y;
-                    Bs[buf][kh + 2][kr] = b[h].z; Bs[buf][kh + 3][kr] = b[h].w;
+                    const int c = col(kh, kr);
+                    Bs[buf][kh][c] = b[h].x; Bs[buf][kh + 1][c] = b[h].y;
+                    Bs[buf][kh + 2][c] = b[h].z; Bs[buf][kh + 3][c] = b[h].w;
                 } else {
-                    *reinterpret_cast<float4 *>(&Bs[buf][mr][mh]) = b[h];
+                    *reinterpret_cast<float4 *>(&Bs[buf][mr][col(mr, mh)]) = b[h];
                 }
             }
         };
@@ -171,9 +176,10 @@ __global__ void __launch_bounds__(kSimtThreads) simt_kernel(const Params p) {
 #pragma unroll
             for (int q0 = 0; q0 < kSlice / 2; ++q0) {
                 const int q = half * (kSlice / 2) + q0;
-                const ulonglong2 av0 = *reinterpret_cast<const ulonglong2 *>(&As[buf][q][ty * 8]);
-                const ulonglong2 av1 = *reinterpret_cast<const ulonglong2 *>(&As[buf][q][ty * 8 + 4]);
-                const float4 bv = *reinterpret_cast<const float4 *>(&Bs[buf][q][tx * 4]);
+                const int ca = col(q, ty * 8);
+                const ulonglong2 av0 = *reinterpret_cast<const ulonglong2 *>(&As[buf][q][ca]);
+                const ulonglong2 av1 = *reinterpret_cast<const ulonglong2 *>(&As[buf][q][ca + 4]);
+                const float4 bv = *reinterpret_cast<const float4 *>(&Bs[buf][q][col(q, tx * 4)]);
                 const uint64_t ar[4] = {av0.x, av0.y, av1.x, av1.y};
                 const uint64_t br[4] = {f2_splat(bv.x), f2_splat(bv.y), f2_splat(bv.z), f2_splat(bv.w)};
 #pragma unroll
