@@ -51,7 +51,8 @@ int make_gmm_plan(const moe_gmm *d, int64_t rows, GmmPlan *out) {
     p.n = d->n;
     p.k = d->k;
     p.accumulate = d->accumulate;
-    // a wait lasts at most one tile: about half a microsecond for 64 of the contraction, 2 allowed
+    // a wait lasts at most one tile (the clearer's: one tile of the producer's): about half a microsecond for 64 of the
+    // contraction, 2 allowed
     p.timeout_ns = kTimeoutNs + 32ull * (uint64_t)std::max<int64_t>(rows, std::max(d->n, d->k));
     return MOE_OK;
 }

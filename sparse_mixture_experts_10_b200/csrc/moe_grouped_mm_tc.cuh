@@ -164,6 +164,29 @@ struct Tile {
     int c0, nc;                 // contraction start and length
 };
 
+// The clearer's wait for a tile's last slice.  Tiles without one may lie before it, any number of them, so the limit
+// is on the time in which the producer (`moving`: the tile that it is at) takes no step to another tile.
+__device__ __forceinline__ bool wait_while_moving(uint64_t *bar, uint32_t parity, uint64_t timeout_ns,
+                                                  const volatile int *moving) {
+    if (mbar_try_wait(bar, parity)) return true;
+    int seen = *moving;
+    uint64_t t0 = globaltimer_ns();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (globaltimer_ns() - t0 > timeout_ns) {
+            const int now = *moving;
+            if (now == seen) {
+                set_status(kStatusTimeout);
+                return false;
+            }
+            seen = now;
+            t0 = globaltimer_ns();
+        }
+    }
+}
+
 // The order in which groups are worked on: those whose tiles take longest first, so that the blocks' last tiles are
 // short ones (32 experts of 512 +- 22 rows, n 4096, k 7168: 945 us in the groups' own order, 896 us so).  ord[j] is the j-th
 // group, cum its first tile.  By every thread of the block; s_off is complete.  Beyond kOrdered groups the tiles
@@ -293,6 +316,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
     uint64_t *tempty = tfull + 2;      // an accumulator has been read
     uint64_t *drain = tempty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *s_at = reinterpret_cast<volatile int *>(tmem_slot + 1);   // TN: the producer's tile
     int *s_off = reinterpret_cast<int *>(tmem_slot + 4);
     int *s_cum = s_off + p.G + 1;
     int *s_ord = s_cum + p.G + 1;
@@ -316,6 +340,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
         }
         mbar_init(drain, 1);
         fence_mbar_init();
+        *s_at = -1;
         tma_prefetch_desc(&tmM);
         tma_prefetch_desc(&tmN.m[0]);
         if (!kNmn) tma_prefetch_desc(&tmN.m[4]);
@@ -345,6 +370,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
         uint32_t tail_phase = 0;
         for (int i = first; i < total && ok; i += step) {
             const Tile t = tile(i);
+            if (KIND == TN && lane == 0) *s_at = i;
             if (KIND != TN && t.rows <= 0) continue;
             const int f = t.f0 + (int)rank * 128;
             const int half = kPair ? t.nh / 2 : t.nh;   // N rows of an instruction that this CTA loads
@@ -490,7 +516,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
             for (int i = first; i < total; i += step) {
                 const Tile t = tile(i);
                 if (t.nc % 16 == 0) continue;
-                if (!__all_sync(0xffffffffu, mbar_wait(raw, tail_phase, p.timeout_ns))) break;
+                if (!__all_sync(0xffffffffu, wait_while_moving(raw, tail_phase, p.timeout_ns, s_at))) break;
                 tail_phase ^= 1;
                 // up to the next 16: 16-byte pieces of the cleared rows in each chunk of 64 values
                 const int left = t.nc % kSl, n16 = (16 - left % 16) * 8;

@@ -296,6 +296,26 @@ def test_grouped_mm_places_past_32_bits():
     close(dw[1, cols], x.t() @ a[1000:].double(), (rows + 8) * 2.0 ** -23 * (x.abs().t() @ a[1000:].double().abs()))
 
 
+@pytest.mark.gpu
+def test_grouped_mm_ragged_segment_behind_long_ones():
+    """A segment whose length is no multiple of 16 behind one whose tiles take more than a second in all: the wait for
+    its last slice begins with the call and is longer than any bound on one tile's work (2.2e15 operations, 1.6 s
+    at the sustained rate, against 1.008 s).  Entries are -1, 0 and 1, so the sums are exact."""
+    rows, tail, n = 262144, 17, 65536
+    x = torch.empty(rows + tail, n, dtype=BF, device="cuda").random_(0, 3, generator=gen(12)).sub_(1)
+    c = torch.full((2, n, n), float("nan"), dtype=BF, device="cuda")
+    d = moe.make_gmm(moe.MOE_GMM_TN, 2, n, n, moe.MOE_BF16, moe.MOE_BF16)
+    off = torch.tensor([0, rows, rows + tail], dtype=torch.int32, device="cuda")
+    moe.check(moe.moe_grouped_mm(d, x, x, c, off, rows + tail))
+    assert status_clear() == 0
+    last = x[rows:].float()
+    for i in range(0, n, 8192):
+        assert torch.equal(c[1, i:i + 8192].float(), last[:, i:i + 8192].t() @ last)
+    for i, j in ((0, 0), (0, n - 128), (n - 128, 4096), (n - 128, n - 128), (32768, 32640)):
+        ref = x[:rows, i:i + 128].double().t() @ x[:rows, j:j + 128].double()
+        assert torch.equal(c[0, i:i + 128, j:j + 128], ref.to(BF))
+
+
 def test_grouped_mm_refusals():
     ok = dict(kind=0, groups=4, n=64, k=64)
 
