@@ -107,7 +107,7 @@ int make_map_mn(CUtensorMap *m, const void *base, int64_t G, int64_t rows, int64
     return make_map_nd(m, 4, base, d, st, b);
 }
 
-template <int KIND, typename TO>
+template <int KIND, typename TO, bool kSums>
 int launch_gmm_tc(gmm::Params p, const DeviceInfo &dev, cudaStream_t s) {
     CUtensorMap mm;
     gmm::NMaps mn;
@@ -128,8 +128,8 @@ int launch_gmm_tc(gmm::Params p, const DeviceInfo &dev, cudaStream_t s) {
     //  wide pairs (256 x 512) where segments have more than 256 rows: 675 us against 714 us; 300 rows 482 against 556
     auto row_tiles = [&](int64_t unit) { return std::max(live, cdiv(p.rows, unit)); };
     const bool pair = (KIND == gmm::TN ? p.G * cdiv(p.n, 256) : row_tiles(256)) * cdiv(F, 256) >= dev.pair_clusters;
-    // (they need both accumulators, and registers cannot hold an fp32 result's running sums of 512 rows)
-    const bool wide = pair && KIND != gmm::TN && sizeof(TO) == 2 && p.rows > 256 * live &&
+    // (they need both accumulators, and registers cannot hold the running sums of 512 rows)
+    const bool wide = pair && KIND != gmm::TN && !kSums && p.rows > 256 * live &&
                       row_tiles(512) * cdiv(F, 256) >= dev.pair_clusters;
     const int unit = pair ? 256 : 128;
     p.m_tiles = (int)cdiv(F, unit);
@@ -141,20 +141,26 @@ int launch_gmm_tc(gmm::Params p, const DeviceInfo &dev, cudaStream_t s) {
     const size_t smem = gmm::tc_smem_bytes(p.G);
     if (pair) {
         const dim3 grid((unsigned)(2 * std::min<int64_t>(upper, dev.pair_clusters)));
-        if constexpr (KIND != gmm::TN && sizeof(TO) == 2)
+        if constexpr (KIND != gmm::TN && !kSums)
             if (wide)
-                return launch_pdl(gmm::tc_pair_kernel<KIND, TO, true>, grid, dim3(gmm::kTcThreads), smem, s, mm, mn, p);
-        return launch_pdl(gmm::tc_pair_kernel<KIND, TO, false>, grid, dim3(gmm::kTcThreads), smem, s, mm, mn, p);
+                return launch_pdl(gmm::tc_pair_kernel<KIND, TO, true, false>, grid, dim3(gmm::kTcThreads), smem, s, mm, mn,
+                                  p);
+        return launch_pdl(gmm::tc_pair_kernel<KIND, TO, false, kSums>, grid, dim3(gmm::kTcThreads), smem, s, mm, mn, p);
     }
-    return launch_pdl(gmm::tc_single_kernel<KIND, TO>, dim3((unsigned)std::min<int64_t>(upper, dev.sms)),
+    return launch_pdl(gmm::tc_single_kernel<KIND, TO, kSums>, dim3((unsigned)std::min<int64_t>(upper, dev.sms)),
                       dim3(gmm::kTcThreads), smem, s, mm, mn, p);
 }
 
 template <int KIND>
 int launch_gmm(const moe_gmm *d, const gmm::Params &p, const DeviceInfo &dev, cudaStream_t s) {
     if (d->dtype == MOE_F32) return launch_gmm_simt<KIND>(p, dev, s);
-    if (d->out_dtype == MOE_F32) return launch_gmm_tc<KIND, float>(p, dev, s);
-    return launch_gmm_tc<KIND, __nv_bfloat16>(p, dev, s);
+    if (d->out_dtype == MOE_F32) return launch_gmm_tc<KIND, float, true>(p, dev, s);
+    // running sums for a bf16 result where a contraction may be longer than a run (segments are known on the device only):
+    // without them 32 weight gradients of 7168 x 2048 over 16448 rows take 450 us, with them 473 us; 8 of 2880 x 1000
+    // over 16640 rows 87 and 89 us; 4 x 2048 x 16448 over 4096 rows 312 us either way
+    const int64_t terms = KIND == gmm::NT ? p.k : KIND == gmm::NN ? p.n : p.rows;   // of a sum, at most
+    if (terms > gmm::kRunBf16 * gmm::kSl) return launch_gmm_tc<KIND, __nv_bfloat16, true>(p, dev, s);
+    return launch_gmm_tc<KIND, __nv_bfloat16, false>(p, dev, s);
 }
 
 // ---------------------------------------------------------------- 8-bit checkpoints
@@ -298,15 +304,17 @@ int launch_q4(int format, const q4::MatvecParams &p, const DeviceInfo &dev, cuda
 // Attributes of this file's kernels, set once per device with the others'.
 int expert_ops_attrs() {
 #define MOE_GMM_ATTR(KIND)                                                     \
-    MOE_TRY(allow_smem(gmm::tc_pair_kernel<KIND, float, false>));              \
-    MOE_TRY(allow_smem(gmm::tc_single_kernel<KIND, float>));                   \
-    MOE_TRY(allow_smem(gmm::tc_pair_kernel<KIND, __nv_bfloat16, false>));      \
-    MOE_TRY(allow_smem(gmm::tc_single_kernel<KIND, __nv_bfloat16>))
+    MOE_TRY(allow_smem(gmm::tc_pair_kernel<KIND, float, false, true>));        \
+    MOE_TRY(allow_smem(gmm::tc_single_kernel<KIND, float, true>));             \
+    MOE_TRY(allow_smem(gmm::tc_pair_kernel<KIND, __nv_bfloat16, false, true>)); \
+    MOE_TRY(allow_smem(gmm::tc_single_kernel<KIND, __nv_bfloat16, true>));     \
+    MOE_TRY(allow_smem(gmm::tc_pair_kernel<KIND, __nv_bfloat16, false, false>)); \
+    MOE_TRY(allow_smem(gmm::tc_single_kernel<KIND, __nv_bfloat16, false>))
     MOE_GMM_ATTR(gmm::NT);
     MOE_GMM_ATTR(gmm::NN);
     MOE_GMM_ATTR(gmm::TN);
-    MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NT, __nv_bfloat16, true>));
-    MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NN, __nv_bfloat16, true>));
+    MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NT, __nv_bfloat16, true, false>));
+    MOE_TRY(allow_smem(gmm::tc_pair_kernel<gmm::NN, __nv_bfloat16, true, false>));
 #undef MOE_GMM_ATTR
     MOE_TRY(allow_smem(q4::matvec_kernel<q4::INT4, 5>));
     MOE_TRY(allow_smem(q4::matvec_kernel<q4::INT4, 6>));

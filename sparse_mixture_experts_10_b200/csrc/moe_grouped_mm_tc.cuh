@@ -53,15 +53,19 @@ constexpr int kOpBytes = 128 * kSl * 2; // 128 values of either side of a slice
 // rows each: 208 us with 8 warps, 167 us with 16).
 constexpr int kEpi = 16;
 constexpr int kTcThreads = 32 * (kEpi + 3);
-// The tensor core's fp32 accumulation drops what is behind the last bit, always towards zero: measured against 64
-// bits, the result comes out small by 8e-10 of itself for every term (4.4e-6 after 4096, 1.9e-5 after 16384).
-// A bf16 result (2^-9) does not show it.  For an fp32 result the contraction is cut into equal runs of at most 12
-// slices (768 terms, 6e-7); the accumulator is read after each and added, rounded to nearest, to running sums in
-// registers.
-constexpr int kRun = 12;
+// The tensor core's fp32 accumulation drops what is behind the last bit, always towards zero: less than 2^-23 of the
+// partial sum for each step of 16 terms.  Measured against 64 bits, a result of terms of both signs comes out small by
+// 8e-10 of itself for every term (4.4e-6 after 4096, 1.9e-5 after 16384), one of 2^23 positive terms by 5%.  So a long
+// contraction is cut into equal runs (kSums); the accumulator is read after each and added, rounded to nearest, to
+// running sums in registers:
+//   fp32 results  runs of at most 12 slices (768 terms, 6e-7)
+//   bf16 results  runs of at most 256 slices (16384 terms, 1.2e-4 at worst beside the 2^-8 of their own rounding);
+//                 up to there they are read once and need no running sums
+constexpr int kRunF32 = 12, kRunBf16 = 256;
 template <bool kF32>
 __device__ __forceinline__ int run_length(int nkb) {
-    if (!kF32 || nkb <= kRun) return nkb;
+    constexpr int kRun = kF32 ? kRunF32 : kRunBf16;
+    if (nkb <= kRun) return nkb;
     const int runs = (nkb + kRun - 1) / kRun;
     return (nkb + runs - 1) / runs;
 }
@@ -275,14 +279,15 @@ __device__ __forceinline__ void store_f32(float *dst, int64_t ldc, bool f_ok, co
     for (int j = 0; j < N; ++j)
         if (j < rows && f_ok) dst[j * ldc] = accumulate ? dst[j * ldc] + v[j] : v[j];
 }
-__device__ __forceinline__ void store_bf16(__nv_bfloat16 *out, int64_t ldc, int f, bool f_ok, const uint32_t (&r)[32],
+template <int N>
+__device__ __forceinline__ void store_bf16(__nv_bfloat16 *out, int64_t ldc, int f, bool f_ok, const float (&v)[N],
                                            int rows, int accumulate) {
     const int odd = threadIdx.x & 1;
     __nv_bfloat16 *dst = out + (f & ~1) + (odd ? ldc : 0);
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {   // even lanes write row j, odd lanes row j + 1
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? r[j] : r[j + 1], 1);
-        float lo = __uint_as_float(odd ? got : r[j]), hi = __uint_as_float(odd ? r[j + 1] : got);
+    for (int j = 0; j < N; j += 2) {   // even lanes write row j, odd lanes row j + 1
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+        float lo = odd ? got : v[j], hi = odd ? v[j + 1] : got;
         if (j + odd < rows && f_ok) {
             uint32_t *q = reinterpret_cast<uint32_t *>(dst + j * ldc);
             if (accumulate) {
@@ -295,11 +300,12 @@ __device__ __forceinline__ void store_bf16(__nv_bfloat16 *out, int64_t ldc, int 
     }
 }
 
-template <int KIND, typename TO, bool kPair, bool kWide>
+template <int KIND, typename TO, bool kPair, bool kWide, bool kSums>
 __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN, const Params &p) {
     pdl_enter();
     constexpr bool kF32 = sizeof(TO) == 4;
-    static_assert(!kWide || (kPair && KIND != TN && !kF32), "wide tiles: CTA pairs, K-major N operand, bf16 results");
+    static_assert(kSums || !kF32, "fp32 results have running sums");
+    static_assert(!kWide || (kPair && KIND != TN && !kSums), "wide tiles: CTA pairs, K-major N operand, one run");
     constexpr int kAccCols = kPair ? 256 : 128;
     constexpr int kStages = ring_stages(KIND, kWide), kNBytes = (kWide ? 2 : 1) * kOpBytes;
     constexpr bool kMmn = KIND != NT, kNmn = KIND == TN;   // MN-major operands
@@ -441,7 +447,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
                 if (KIND == TN ? t.nc == 0 : t.rows <= 0) continue;
                 const uint32_t idesc = kIdesc | (static_cast<uint32_t>(t.nh >> 3) << 17);
                 const int nkb = (t.nc + kSl - 1) / kSl;
-                const int run = run_length<kF32>(nkb);
+                const int run = kSums ? run_length<kF32>(nkb) : nkb;
                 for (int kb = 0, end = 0; kb < nkb && ok;) {
                     end = min(nkb, kb + run);
                     const int a0 = kWide ? 0 : local & 1;
@@ -556,7 +562,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
                 }
             };
             const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-            if constexpr (kF32) {
+            if constexpr (kSums) {
                 // running sums of this warp's columns
                 constexpr int kCols = kAccCols / 4, kC16 = kCols / 16;
                 const int c0 = part * kCols, nkb = (t.nc + kSl - 1) / kSl, run = run_length<kF32>(nkb);
@@ -587,9 +593,12 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
                 }
                 if (!ok) break;
 #pragma unroll
-                for (int c = 0; c < kC16; ++c)
-                    store_f32<16>(out + (c0 + c * 16) * p.ldc + f, p.ldc, f_ok, sum[c], t.rows - c0 - c * 16,
-                                  KIND == TN ? p.accumulate : 0);
+                for (int c = 0; c < kC16; ++c) {
+                    TO *dst = out + (c0 + c * 16) * p.ldc;
+                    const int rows = t.rows - c0 - c * 16, accumulate = KIND == TN ? p.accumulate : 0;
+                    if constexpr (kF32) store_f32<16>(dst + f, p.ldc, f_ok, sum[c], rows, accumulate);
+                    else store_bf16<16>(dst, p.ldc, f, f_ok, sum[c], rows, accumulate);
+                }
             } else {
                 const int a0 = kWide ? 0 : local & 1;
                 const uint32_t ph = kWide ? local & 1 : (local >> 1) & 1;
@@ -603,7 +612,10 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
                         uint32_t r[32];
                         tmem_ld_32x32b_x32(lanes + (a0 + h) * kAccCols + c, r);
                         tmem_ld_wait();
-                        store_bf16(dst + c * p.ldc, p.ldc, f, f_ok, r, rows - c, KIND == TN ? p.accumulate : 0);
+                        float v[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
+                        store_bf16<32>(dst + c * p.ldc, p.ldc, f, f_ok, v, rows - c, KIND == TN ? p.accumulate : 0);
                     }
                     release(a0 + h);
                 }
@@ -620,15 +632,15 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
     }
 }
 
-template <int KIND, typename TO, bool kWide>
+template <int KIND, typename TO, bool kWide, bool kSums>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     tc_pair_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_constant__ NMaps tmN, const Params p) {
-    tc_body<KIND, TO, true, kWide>(tmM, tmN, p);
+    tc_body<KIND, TO, true, kWide, kSums>(tmM, tmN, p);
 }
-template <int KIND, typename TO>
+template <int KIND, typename TO, bool kSums>
 __global__ void __launch_bounds__(kTcThreads, 1)
     tc_single_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_constant__ NMaps tmN, const Params p) {
-    tc_body<KIND, TO, false, false>(tmM, tmN, p);
+    tc_body<KIND, TO, false, false, kSums>(tmM, tmN, p);
 }
 
 }  // namespace gmm

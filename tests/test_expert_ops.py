@@ -169,6 +169,39 @@ def test_grouped_mm_long_sums_in_fp32(kind):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("terms,other", [(1 << 23, 8), (40008, 72)])
+def test_grouped_mm_long_sums_in_bf16(kind, terms, other):
+    """bf16 results of sums without cancellation: runs of at most 16384 terms, 16 a step, each step off by at most
+    2^-23 of a partial sum, then a rounding of 2^-24 for every run's addition."""
+    g = gen(44)
+    tn = kind == moe.MOE_GMM_TN
+    n, k = (other, other) if tn else (other, terms) if kind == moe.MOE_GMM_NT else (terms, other)
+    rows = terms if tn else other + 1
+    a = randn(g, rows, k if kind == moe.MOE_GMM_NT else n).abs()
+    b = (randn(g, rows, k) if tn else randn(g, 1, n, k)).abs()
+    c = torch.empty(*((1, n) if tn else (rows,)), n if kind == moe.MOE_GMM_NT else k, dtype=BF, device="cuda")
+    d = moe.make_gmm(kind, 1, n, k, moe.MOE_BF16, moe.MOE_BF16)
+    moe.check(moe.moe_grouped_mm(d, a, b, c, torch.tensor([0, rows], dtype=torch.int32, device="cuda"), rows))
+    assert status_clear() == 0
+    ref, S = gmm_reference(kind, a, b, [0, rows], c.shape)
+    close(c, ref, (16384 / 16 + terms / 16384 / 2 + 8) * 2.0 ** -23 * S)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+def test_grouped_mm_long_sums_in_bf16_beside_short_ones(kind):
+    """Several runs and a single one, in CTA pairs; row strides; a weight gradient that is added to."""
+    if kind == moe.MOE_GMM_TN:
+        for accumulate in (False, True):
+            gmm_case(kind, [20000, 0, 33, 1500], 1288, 1280, BF, BF, seed=45, start=2, extra=9, pads=(8, 16, 24),
+                     accumulate=accumulate)
+    else:
+        n, k = (2048, 16648) if kind == moe.MOE_GMM_NT else (16648, 2048)
+        gmm_case(kind, [300, 0, 2300, 33], n, k, BF, BF, seed=46, start=2, extra=9, pads=(8, 16, 24))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
 def test_grouped_mm_graph_follows_new_offsets(kind):
     """A captured call reads its offsets when it is replayed: any other segments of as many rows."""
     n, k, rows = 136, 200, 400
