@@ -398,11 +398,12 @@ int moe_backward(const moe_config *cfg, const void *x, int64_t T, const moe_weig
  *               zero for a group without rows
  * bf16 operands give bf16 or fp32 results, fp32 operands fp32 ones; sums are
  * held in fp32 and rounded once at the end.  With bf16 operands the tensor core
- * forms them, which drops up to 2^-23 of the partial sum, towards zero, for
- * every 16 terms; every 768 terms (bf16 results: 16384) at most the partial sum
- * is added, rounded to nearest, to the whole one and begins anew.  So the drop
- * stays below 6e-6 (bf16 results: 1.3e-4) of sum |a b|, however long the sum is;
- * measured 5e-7 for terms of both signs (bf16 results: 1.7e-5 after 14336). */
+ * forms them, which drops bits towards zero: less than 5 * 2^-23 of the largest
+ * partial sum for every 16 terms.  After at most 768 terms (bf16 results: 16384)
+ * the partial sum is added, rounded to nearest, to the whole one and begins
+ * anew, so that the loss stays below 2.9e-5 (bf16 results: 6.2e-4) of sum |a b|
+ * however long the sum is; measured 1.3e-6 of the result for terms of one sign,
+ * 5e-7 for both signs (bf16 results: 1.7e-5 after 14336 terms). */
 enum { MOE_GMM_NT = 0, MOE_GMM_NN = 1, MOE_GMM_TN = 2 };
 typedef struct {
     int32_t kind;       /* MOE_GMM_* */

@@ -53,14 +53,15 @@ constexpr int kOpBytes = 128 * kSl * 2; // 128 values of either side of a slice
 // rows each: 208 us with 8 warps, 167 us with 16).
 constexpr int kEpi = 16;
 constexpr int kTcThreads = 32 * (kEpi + 3);
-// The tensor core's fp32 accumulation drops what is behind the last bit, always towards zero: less than 2^-23 of the
-// partial sum for each step of 16 terms.  Measured against 64 bits, a result of terms of both signs comes out small by
-// 8e-10 of itself for every term (4.4e-6 after 4096, 1.9e-5 after 16384), one of 2^23 positive terms by 5%.  So a long
-// contraction is cut into equal runs (kSums); the accumulator is read after each and added, rounded to nearest, to
-// running sums in registers:
-//   fp32 results  runs of at most 12 slices (768 terms, 6e-7)
-//   bf16 results  runs of at most 256 slices (16384 terms, 1.2e-4 at worst beside the 2^-8 of their own rounding);
-//                 up to there they are read once and need no running sums
+// The tensor core's fp32 accumulation drops bits, always towards zero: of each step's 16 products what is below 2^-25
+// of the largest exponent in the sum, and of their sum what is below 2^-23 (seen with sums built of powers of two), so
+// less than 16 * 2^-25 + 2^-23 = 5 * 2^-23 of the partial sum a step.  Measured against 64 bits, a result of terms of
+// both signs comes out small by 8e-10 of itself for every term (4.4e-6 after 4096, 1.9e-5 after 16384), one of 2^23
+// positive terms by 5%.  So a long contraction is cut into equal runs (kSums); the accumulator is read after each and
+// added, rounded to nearest, to running sums in registers:
+//   fp32 results  runs of at most 12 slices (768 terms: 6e-7, positive terms 1.3e-6)
+//   bf16 results  runs of at most 256 slices (16384 terms: below 1024 * 5 * 2^-23 = 6.2e-4, beside up to 2^-8 of their
+//                 own rounding); up to there they are read once and need no running sums
 constexpr int kRunF32 = 12, kRunBf16 = 256;
 template <bool kF32>
 __device__ __forceinline__ int run_length(int nkb) {
