@@ -42,10 +42,9 @@ int make_gmm_plan(const moe_gmm *d, int64_t rows, GmmPlan *out) {
     MOE_TRY(take_stride(d->lda, out->a_cols, es, &p.lda));
     MOE_TRY(take_stride(d->ldb, d->k, es, &p.ldb));
     MOE_TRY(take_stride(d->ldc, out->c_cols, os, &p.ldc));
-    // a tensor map's strides stay below 2^40 bytes
-    if ((int64_t)d->n * p.ldb * es >= (int64_t(1) << 40) || p.lda * es >= (int64_t(1) << 40) ||
-        (int64_t)d->n * p.ldc * os >= (int64_t(1) << 40))
-        return MOE_ERR_UNSUPPORTED;
+    // a tensor map's strides stay below 2^40 bytes (by division: n rows of ld may pass 64 bits)
+    const int64_t most = (int64_t(1) << 40) - 1;
+    if (p.ldb > most / es / d->n || p.ldc > most / os / d->n) return MOE_ERR_UNSUPPORTED;
     p.rows = rows;
     p.G = d->groups;
     p.n = d->n;

@@ -373,6 +373,14 @@ def test_grouped_mm_refusals():
     assert rc(rows=0, kind=moe.MOE_GMM_TN, c=None) in BAD
 
 
+def test_grouped_mm_refuses_weights_beyond_64_bits():
+    """n rows of ldb (ldc) elements whose bytes pass 2^63 and come out small or negative when multiplied."""
+    for kind, ld in ((moe.MOE_GMM_NT, "ldb"), (moe.MOE_GMM_NN, "ldb"), (moe.MOE_GMM_TN, "ldc")):
+        for n, s in ((2 ** 31 - 8, 2 ** 32), (2 ** 31 - 8, 2 ** 32 - 8), (2 ** 30, 2 ** 32)):
+            d = moe.make_gmm(kind, 4, n, 64, accumulate=kind == moe.MOE_GMM_TN, **{ld: s})
+            assert moe.moe_grouped_mm(d, None, None, None, None, 0, 0) == moe.MOE_ERR_UNSUPPORTED, (kind, n, s)
+
+
 @pytest.mark.gpu
 def test_grouped_mm_without_rows_clears_weight_gradients():
     c = torch.ones(3, 16, 24, device="cuda")
