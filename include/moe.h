@@ -416,8 +416,10 @@ typedef struct {
                            out_dtype), 0 overwrites it */
     int32_t reserved;   /* 0 */
     int64_t lda, ldb, ldc; /* row strides in elements, 0 = contiguous; a
-                           multiple of 16 bytes.  A group's weights (b, or c of
-                           MOE_GMM_TN) are n such rows and follow each other. */
+                           multiple of 16 bytes, at most 2^32 elements.  A
+                           group's weights (b, or c of MOE_GMM_TN) are n such
+                           rows, below 2^40 bytes (else MOE_ERR_UNSUPPORTED), and
+                           follow each other. */
 } moe_gmm;
 /* row_offsets [groups + 1] int32 (device), non-decreasing, within 0..rows;
  * rows: the rows that a (MOE_GMM_TN: a and b) holds.  Rows outside every

@@ -42,9 +42,10 @@ int make_gmm_plan(const moe_gmm *d, int64_t rows, GmmPlan *out) {
     MOE_TRY(take_stride(d->lda, out->a_cols, es, &p.lda));
     MOE_TRY(take_stride(d->ldb, d->k, es, &p.ldb));
     MOE_TRY(take_stride(d->ldc, out->c_cols, os, &p.ldc));
-    // a tensor map's strides stay below 2^40 bytes (by division: n rows of ld may pass 64 bits)
+    // a tensor map's strides stay below 2^40 bytes: a group's weights are n rows of ldb (by division: their product may
+    // pass 64 bits); the weight gradient's n rows of ldc keep to it too, so that no index of c does
     const int64_t most = (int64_t(1) << 40) - 1;
-    if (p.ldb > most / es / d->n || p.ldc > most / os / d->n) return MOE_ERR_UNSUPPORTED;
+    if (d->kind == MOE_GMM_TN ? p.ldc > most / os / d->n : p.ldb > most / es / d->n) return MOE_ERR_UNSUPPORTED;
     p.rows = rows;
     p.G = d->groups;
     p.n = d->n;

@@ -381,6 +381,30 @@ def test_grouped_mm_refuses_weights_beyond_64_bits():
             assert moe.moe_grouped_mm(d, None, None, None, None, 0, 0) == moe.MOE_ERR_UNSUPPORTED, (kind, n, s)
 
 
+def test_grouped_mm_limits_weights_only():
+    """The limit of 2^40 bytes is one on a group's weights: n rows of the other operands are not a thing."""
+    for kind, n, k, kw in ((moe.MOE_GMM_NT, 2 ** 20, 64, {}), (moe.MOE_GMM_NN, 2 ** 20, 64, dict(ldc=2 ** 19)),
+                           (moe.MOE_GMM_TN, 2 ** 20, 64, dict(ldb=2 ** 19, accumulate=True))):
+        d = moe.make_gmm(kind, 4, n, k, **kw)
+        assert moe.moe_grouped_mm(d, None, None, None, None, 0, 0) == moe.MOE_OK, kind
+
+
+@pytest.mark.gpu
+def test_grouped_mm_wide_results():
+    """Rows of 2^20 results of a short contraction."""
+    rows, n, k = 40, 2 ** 20, 64
+    a, b = randn(gen(47), rows, k), randn(gen(48), 1, n, k)
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    for dt in (BF, F32):
+        c = torch.full((rows, n), float("nan"), dtype=dt, device="cuda")
+        x, w = a.to(dt), b.to(dt)
+        d = moe.make_gmm(moe.MOE_GMM_NT, 1, n, k, moe.dtype_code(dt), moe.dtype_code(dt))
+        moe.check(moe.moe_grouped_mm(d, x, w, c, off, rows))
+        assert status_clear() == 0
+        ref, S = gmm_reference(moe.MOE_GMM_NT, a, b, [0, rows], c.shape)
+        close(c, ref, (k + 8) * 2.0 ** -23 * S)
+
+
 @pytest.mark.gpu
 def test_grouped_mm_without_rows_clears_weight_gradients():
     c = torch.ones(3, 16, 24, device="cuda")
