@@ -159,25 +159,26 @@ __device__ __forceinline__ float amax_group(const uint32_t (&raw)[4], int lanes)
     return __uint_as_float(m);
 }
 
-// Phi(v), the normal distribution function, with its density, and the sigmoid, in the accuracy of the row type:
-// fp32 rows take erff, expf and a division.  bf16 rows (rounded to 2^-8 afterwards) take the special-function
-// unit: Phi(-|v|) = t (b1 + t (b2 + ...)) exp(-v^2 / 2), t = 1 / (1 + p |v| / sqrt 2), Abramowitz & Stegun,
-// Handbook of Mathematical Functions, formula 7.1.26 (absolute error of Phi at most 0.75e-7), whose
-// exponential is the density's too.
+// Phi(v), the normal distribution function, with its density, and the sigmoid, in the accuracy of the row type, for
+// v < 0 relative to Phi itself: fp32 rows take erfcf, expf and a division.  bf16 rows (rounded to 2^-8 afterwards)
+// take the special-function unit: Phi(-|v|) = t (q1 + t (q2 + ... + t q6)) exp(-v^2 / 2), t = 1 / (1 + c |v|), whose
+// exponential is the density's too.  c and q are a fit of Phi(-x) exp(x^2 / 2) for x from 0 to 13.5 (Phi(-13.2) is
+// 2^-130) that minimises the larger of error / 7.5e-8 and relative error / 2^-11: it is off by at most 3e-8 and by at
+// most 2^-12.3 of Phi; the rounding of t and of the exponential adds up to 4e-7 near 0.
 template <typename T>
 __device__ __forceinline__ float phi(float v, float *density) {
     constexpr float kDensity0 = 0.39894228040143268f;   // 1 / sqrt(2 pi)
     if (sizeof(T) == 4) {
         if (density) *density = expf(-0.5f * v * v) * kDensity0;
-        return 0.5f * (1.0f + erff(v * 0.70710678118654752f));
+        return normal_cdf(v);
     }
-    const float a = fabsf(v);
-    const float t = rcp_approx(fmaf(a, 0.2316418882663604f, 1.0f));   // p / sqrt 2, p = 0.3275911
+    const float t = rcp_approx(fmaf(fabsf(v), 0.287f, 1.0f));
     const float e = ex2_approx(v * v * -0.7213475204444817f);         // log2(e) / 2
-    float q = fmaf(t, 0.5307027145f, -0.7265760135f);                 // a_i / 2
-    q = fmaf(t, q, 0.7107068705f);
-    q = fmaf(t, q, -0.142248368f);
-    q = fmaf(t, q, 0.127414796f);
+    float q = fmaf(t, -0.0936281755566597f, 0.3131586015224457f);
+    q = fmaf(t, q, -0.12920913100242615f);
+    q = fmaf(t, q, 0.19976626827690674f);
+    q = fmaf(t, q, 0.09363754838705063f);
+    q = fmaf(t, q, 0.11627483367919922f);
     const float below = q * t * e;
     if (density) *density = e * kDensity0;
     return v < 0.f ? below : 1.0f - below;

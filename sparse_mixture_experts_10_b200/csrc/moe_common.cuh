@@ -317,6 +317,9 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+// The normal distribution function; 1 + erff would cancel for v < 0 (0 from -5.6 down).
+__device__ __forceinline__ float normal_cdf(float v) { return 0.5f * erfcf(v * -0.70710678118654752f); }
+
 // Special-function unit: 1/x and 2^x (hardware approximations, relative
 // error about 2^-22; subnormal results flush to zero).
 __device__ __forceinline__ float rcp_approx(float x) {

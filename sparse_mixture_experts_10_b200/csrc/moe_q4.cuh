@@ -53,7 +53,7 @@ __device__ __forceinline__ float wide_scale(uint32_t b) {
 template <int FMT>
 __device__ __forceinline__ float scale_of(const void *s, int64_t i) { return wide_scale<FMT>(raw_scale<FMT>(s, i)); }
 
-__device__ __forceinline__ float gelu(float v) { return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f)); }
+__device__ __forceinline__ float gelu(float v) { return v * normal_cdf(v); }
 __device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
 
 // ---------------------------------------------------------------- the products

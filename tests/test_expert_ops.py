@@ -578,6 +578,45 @@ def test_ckpt_backward_matches_differences(act):
         assert abs(float(dw[r]) - num) <= 1e-5 * (1 + abs(num))
 
 
+def cdf_err(v, dt):
+    """Relative error of the computed Phi for v < 0, where a small value is no difference of large ones.
+    fp32: erfc's argument is off by 2^-23 of itself (constant and product) and x erfc'(x) / erfc(x) is below
+    v^2 + 1.5 |v| there, erfcf is off by at most 4 steps, the products by 2.  bf16: the fit's 2^-12.3, the
+    exponent's 2^-23 v^2 / 2 (v^2 of an 8-bit value is exact) and 2^-18 of the special-function unit and the sum:
+    below 1.1 2^-12 down to v = -13.2."""
+    return 2.0 ** -23 * (v * v + 1.5 * v.abs() + 6) if dt == F32 else torch.full_like(v, 1.1 * 2.0 ** -12)
+
+
+def cdf(v):
+    """Phi in 64 bits; torch.special.ndtr is 0 on the device from -8.3 down, where Phi is 5e-17."""
+    return 0.5 * torch.special.erfc(v * -math.sqrt(0.5))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_ckpt_gelu_of_negative_values_keeps_its_relative_error(dt):
+    """h, w h and its derivative from -1 to -13 (each group of the checkpoint has values of one size)."""
+    width, rows = 1536, 3
+    u = -torch.linspace(1, 13, rows * width, device="cuda").view(rows, width).to(dt)
+    d = moe.make_ckpt(width, moe.MOE_ACT_GELU, moe.dtype_code(dt), moe.MOE_CKPT_INT8, 32)
+    h, q, s = run_forward(d, u, rows, width, moe.MOE_CKPT_INT8, 32, 1)
+    x = u.to(F64)
+    ref = x * cdf(x)
+    close(h, ref, ref.abs() * cdf_err(x, dt))
+    v = torch.empty(rows, width, device="cuda")
+    moe.check(moe.moe_ckpt_load(moe.make_ckpt(width, moe.MOE_ACT_GELU, moe.MOE_F32, moe.MOE_CKPT_INT8, 32), q, s, rows, v))
+    v = v.to(F64)
+    dh, w = torch.ones(rows, width, dtype=dt, device="cuda"), torch.tensor([1.0, 0.5, 2.0], device="cuda")
+    du, hw = torch.empty_like(u), torch.empty_like(u)
+    moe.check(moe.moe_ckpt_backward(d, q, s, rows, dh, w, du, hw, None))
+    assert status_clear() == 0
+    wt, below = w.to(F64)[:, None], cdf(v)
+    close(hw, wt * v * below, wt * (v * below).abs() * (cdf_err(v, dt) + 2.0 ** -23))
+    slope = v * torch.exp(-0.5 * v * v) / math.sqrt(2 * math.pi)   # v times the density, off by 2^-23 (v^2 / 2 + 8)
+    close(du, wt * (below + slope), wt * (below * cdf_err(v, dt) + slope.abs() * 2.0 ** -23 * (v * v / 2 + 8) +
+                                        (below + slope).abs() * 2.0 ** -23))
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -895,6 +934,28 @@ def test_q4_matvec_special_scales_and_inputs():
         x[1, 40] = float("inf")
         moe.check(moe.moe_q4_matvec(d, x, 2, 1, e, codes, scales, None, y, moe.MOE_F32))
         assert not torch.isfinite(y[1]).any() and torch.isfinite(y[0]).sum() == n - 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", [BF, F32])
+def test_q4_matvec_gelu_of_negative_products_keeps_its_relative_error(out):
+    """A matrix of ones and zeros passes x[0] on exactly: GELU of each bf16 value from -1 to -13."""
+    n, k = 16, 32
+    v = -torch.linspace(1, 13, 400, device="cuda").to(BF).unique()
+    pairs = v.numel()
+    x = torch.zeros(pairs, k, dtype=BF, device="cuda")
+    x[:, 0] = v
+    codes = torch.full((1, n, k // 2), 0x88, dtype=torch.uint8, device="cuda")
+    codes[..., 0] = 0x89   # 1, then zeros
+    scales = torch.ones(1, n, 1, dtype=BF, device="cuda")
+    y = torch.empty(pairs, n, dtype=out, device="cuda")
+    d = moe.make_q4(1, n, k, 32, moe.MOE_Q4_INT4, moe.MOE_ACT_GELU)
+    e = torch.zeros(pairs, dtype=torch.int32, device="cuda")
+    moe.check(moe.moe_q4_matvec(d, x, pairs, 1, e, codes, scales, None, y, moe.dtype_code(out)))
+    assert status_clear() == 0
+    a = v.to(F64)[:, None].expand(pairs, n)
+    ref = a * cdf(a)
+    close(y, ref, ref.abs() * cdf_err(a, F32))
 
 
 @pytest.mark.gpu
