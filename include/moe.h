@@ -487,9 +487,12 @@ int moe_ckpt_backward(const moe_ckpt *d, const uint8_t *q, const uint8_t *scales
 enum { MOE_Q4_INT4 = 0, MOE_Q4_E2M1 = 1 };
 typedef struct {
     int32_t experts; /* 1..1024 */
-    int32_t n;       /* rows of an expert's matrix: a multiple of 8 (SwiGLU: 16) */
-    int32_t k;       /* a multiple of 32; moe_q4_matvec holds a row of x in shared
-                        memory: beyond about 50 thousand MOE_ERR_UNSUPPORTED */
+    int32_t n;       /* rows of an expert's matrix: a multiple of 8 (SwiGLU: 16),
+                        at most 2^20 */
+    int32_t k;       /* a multiple of 32, at most 2^20; moe_q4_matvec holds a row of
+                        x (512 bytes for every 256 values) beside 4 bytes a pair in
+                        shared memory: up to 41728 with any number of pairs, up to
+                        49920 with at most 64, beyond MOE_ERR_UNSUPPORTED */
     int32_t group;   /* values per scale */
     int32_t format;  /* MOE_Q4_* */
     int32_t act;     /* applied to the products: MOE_ACT_NONE, MOE_ACT_GELU, or

@@ -281,13 +281,12 @@ int launch_q4(int format, const q4::MatvecParams &p, const DeviceInfo &dev, cuda
     }
     // pairs staged at a time and the ring's length: what shared memory holds
     q.x_stride = q4::x_stride(p.k);
-    const size_t room = 227 * 1024 - 32 * 1024;   // 32 KB of static shared memory
+    const size_t room = q4::kRoom;
     q.slots = 4;
     q.cols_pass = (int)std::min<int64_t>(p.pairs, q4::kMaxCols);
     if (q4::matvec_smem(4, q.cols_pass, p.k, p.pairs) > room) q.slots = 3;
     while (q.cols_pass > 1 && q4::matvec_smem(q.slots, q.cols_pass, p.k, p.pairs) > room) --q.cols_pass;
-    const size_t smem = q4::matvec_smem(q.slots, q.cols_pass, p.k, p.pairs);
-    if (smem > room) return MOE_ERR_UNSUPPORTED;
+    const size_t smem = q4::matvec_smem(q.slots, q.cols_pass, p.k, p.pairs);   // one column fits: checked before
     // a copy is four tiles where a block's step has as many: a step at an expert's end then reads little too much
     q.box_tiles = std::min(4, q4::kWarps / q.ks);
     CUtensorMap map;
@@ -470,7 +469,7 @@ int moe_q4_matvec(const moe_q4 *d, const void *x, int64_t pairs, int32_t x_div, 
     q4::MatvecParams p{};
     MOE_TRY(make_q4_params(d, &p));
     if (pairs < 0 || x_div < 1 || !dtype_ok(y_dtype)) return MOE_ERR_INVALID_ARG;
-    if (pairs > q4::kMaxPairs) return MOE_ERR_UNSUPPORTED;
+    if (pairs > q4::kMaxPairs || q4::matvec_smem(3, 1, p.k, pairs) > q4::kRoom) return MOE_ERR_UNSUPPORTED;
     if (pairs == 0) return MOE_OK;
     if (!x || !expert || !codes || !scales || !y) return MOE_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) || !aligned16(y) || !aligned4(expert) || !aligned4(gate))

@@ -548,6 +548,7 @@ __global__ void __launch_bounds__(kThreadsMv, 1)
 // Bytes between staged rows of x: whole chunks of k, and an odd number of 64 bytes, so that the 16-byte reads
 // of two rows hit different banks.
 constexpr uint32_t x_stride(int k) { return (uint32_t)((k + kChunk - 1) / kChunk * kChunk * 2 + 64); }
+constexpr size_t kRoom = 227 * 1024 - 32 * 1024;   // dynamic shared memory: 32 KB are left to the static one
 constexpr size_t matvec_smem(int slots, int cols, int k, int64_t pairs) {
     return 1024 + (size_t)slots * kSlotBytes + (size_t)cols * x_stride(k) + (size_t)pairs * 4;
 }

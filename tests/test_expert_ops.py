@@ -909,6 +909,22 @@ def test_q4_matvec_wide_rows():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("k,pairs", [(41728, 4096), (49920, 64)])
+def test_q4_matvec_widest_rows(k, pairs):
+    """The largest k for the most pairs, and the most pairs for the largest k."""
+    q4_case(2, 16, k, 128, moe.MOE_Q4_INT4, moe.MOE_ACT_NONE, pairs, 8, F32, True, seed=3)
+
+
+def test_q4_matvec_refuses_rows_beyond_shared_memory():
+    """Before anything is asked of a device: one chunk of 256 above the documented limits."""
+    for k, pairs in ((41760, 4096), (49952, 1), (1 << 20, 1)):
+        for fmt in (moe.MOE_Q4_INT4, moe.MOE_Q4_E2M1):
+            d = moe.make_q4(4, 32, k, 32, fmt)
+            rc = moe.moe_q4_matvec(d, 256, pairs, 1, 256, 256, 256, None, 256, moe.MOE_F32, 0)
+            assert rc == moe.MOE_ERR_UNSUPPORTED, (k, pairs, rc)
+
+
+@pytest.mark.gpu
 def test_q4_matvec_special_scales_and_inputs():
     """A NaN scale or an infinite input reaches the results that use it, and no others; e2m1's extreme
     exponents and subnormal int4 scales count."""
