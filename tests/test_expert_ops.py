@@ -295,6 +295,131 @@ def test_grouped_mm_is_reproducible_and_captures(kind):
         assert torch.equal(a, gmm_case(kind, [200, 0, 77, 300], 264, 328, BF, F32, seed=7, run=how))
 
 
+# Segments that take tiles of two accumulators (more than 256 rows a tile) and of one, with rows enough for tiles of
+# 512 rows; each CTA pair works on several of them.
+MIXED = [1500, 0, 700, 17, 900, 260, 200]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", [moe.MOE_GMM_NT, moe.MOE_GMM_NN])
+@pytest.mark.parametrize("width,terms", [(4104, 1000), (4096, 640), (5120, 328), (4224, 2056)])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_grouped_mm_tiles_of_512_rows(kind, width, terms, out):
+    """bf16 results (fp32 ones have tiles of 256 rows) over many slices, in whole chunks of 64 and not, with row
+    strides and NaN outside the operands."""
+    n, k = (width, terms) if kind == moe.MOE_GMM_NT else (terms, width)
+    gmm_case(kind, MIXED, n, k, BF, out, seed=width, start=3, extra=5, pads=(8, 16, 24))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", [moe.MOE_GMM_NT, moe.MOE_GMM_NN])
+def test_grouped_mm_tiles_of_512_rows_in_many_groups(kind):
+    """More groups than are put in order: long and short tiles alternate."""
+    n, k = (2304, 136) if kind == moe.MOE_GMM_NT else (136, 2304)
+    gmm_case(kind, [600, 40] * 66, n, k, BF, BF, seed=9)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("n,k", [(1288, 1352), (1536, 1280)])
+def test_grouped_mm_weight_gradients_of_cta_pairs(out, accumulate, n, k):
+    gmm_case(moe.MOE_GMM_TN, [100, 0, 31, 330, 64, 1, 720], n, k, BF, out, seed=n, start=7, extra=9, pads=(8, 16, 24),
+             accumulate=accumulate)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("out", [BF, F32])
+def test_grouped_mm_infinities_stay_in_their_segment_of_cta_pairs(kind, out):
+    """Segments of NaN rows and experts between others, at borders inside a tile and a slice."""
+    lengths, bad = [300, 9, 700, 64, 433, 50, 600], (1, 3, 5)
+    off = offsets(lengths)
+    n, k = (1288, 1352) if kind == moe.MOE_GMM_TN else (4104, 200) if kind == moe.MOE_GMM_NT else (200, 4104)
+    g = gen(13)
+    tn = kind == moe.MOE_GMM_TN
+    a = randn(g, off[-1], k if kind == moe.MOE_GMM_NT else n)
+    b = randn(g, off[-1], k) if tn else randn(g, len(lengths), n, k)
+    c = torch.empty(*((len(lengths), n) if tn else (off[-1],)), n if kind == moe.MOE_GMM_NT else k, dtype=out, device="cuda")
+    ref, S = gmm_reference(kind, a, b, off, c.shape)
+    for i in bad:
+        a[off[i]:off[i + 1]] = float("inf")
+        (b[off[i]:off[i + 1]] if tn else b[i]).fill_(float("nan"))
+    d = moe.make_gmm(kind, len(lengths), n, k, moe.MOE_BF16, moe.dtype_code(out))
+    moe.check(moe.moe_grouped_mm(d, a, b, c, torch.tensor(off, dtype=torch.int32, device="cuda"), off[-1]))
+    assert status_clear() == 0
+    for i in range(len(lengths)):
+        at = i if tn else slice(off[i], off[i + 1])
+        if i in bad:
+            assert torch.isnan(c[at]).all()
+        else:
+            close(c[at], ref[at], (max(lengths + [n if kind == moe.MOE_GMM_NN else k]) + 8) * 2.0 ** -23 * S[at])
+
+
+def on_side(f):
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        f()
+    torch.cuda.current_stream().wait_stream(s)
+
+
+def in_graph(f):
+    f()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        f()
+    for _ in range(3):
+        graph.replay()
+
+
+def twice_at_once(f):
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        f()
+    f()
+    torch.cuda.current_stream().wait_stream(s)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("out", [BF, F32])
+def test_grouped_mm_of_cta_pairs_is_reproducible_and_captures(kind, out):
+    n, k = (1288, 1352) if kind == moe.MOE_GMM_TN else (4104, 328) if kind == moe.MOE_GMM_NT else (328, 4104)
+    first = gmm_case(kind, MIXED, n, k, BF, out, seed=14)
+    for how in (on_side, in_graph, twice_at_once):
+        assert torch.equal(first, gmm_case(kind, MIXED, n, k, BF, out, seed=14, run=how))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+def test_grouped_mm_of_cta_pairs_follows_new_offsets_in_a_graph(kind):
+    """Replays with other segments of as many rows, other numbers of tiles and of slices to clear."""
+    n, k = (1288, 1352) if kind == moe.MOE_GMM_TN else (4104, 328) if kind == moe.MOE_GMM_NT else (328, 4104)
+    g, rows, tn = gen(15), 3600, kind == moe.MOE_GMM_TN
+    a = randn(g, rows, k if kind == moe.MOE_GMM_NT else n)
+    b = randn(g, rows, k) if tn else randn(g, 7, n, k)
+    c = torch.empty(*((7, n) if tn else (rows,)), n if kind == moe.MOE_GMM_NT else k, dtype=BF, device="cuda")
+    o = torch.tensor(offsets([500] * 6 + [600]), dtype=torch.int32, device="cuda")
+    d = moe.make_gmm(kind, 7, n, k)
+    call = lambda: moe.check(moe.moe_grouped_mm(d, a, b, c, o, rows))
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for lengths in ([0] * 6 + [3600], [3600] + [0] * 6, [1, 1799, 3, 1, 1000, 255, 541], [257, 513, 16, 0, 15, 1, 2798]):
+        off = offsets(lengths)
+        o.copy_(torch.tensor(off, dtype=torch.int32))
+        c.fill_(float("nan"))
+        graph.replay()
+        assert status_clear() == 0
+        ref, S = gmm_reference(kind, a, b, off, c.shape)
+        close(c, ref, (rows + 8) * 2.0 ** -23 * S)
+
+
 @pytest.mark.gpu
 def test_grouped_mm_clamps_offsets_that_break_the_rule():
     d = moe.make_gmm(moe.MOE_GMM_NT, 3, 16, 16, moe.MOE_BF16, moe.MOE_F32)
