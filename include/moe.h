@@ -408,7 +408,8 @@ enum { MOE_GMM_NT = 0, MOE_GMM_NN = 1, MOE_GMM_TN = 2 };
 typedef struct {
     int32_t kind;       /* MOE_GMM_* */
     int32_t groups;     /* 1..1024 */
-    int32_t n, k;       /* multiples of 8 (bf16) or 4 (fp32) */
+    int32_t n, k;       /* multiples of 8 (bf16) or 4 (fp32); they and the rows of
+                           a call at most 2^31 - 1025 */
     int32_t dtype;      /* of a and b: MOE_F32 or MOE_BF16 */
     int32_t out_dtype;  /* of c */
     int32_t accumulate; /* MOE_GMM_TN only: 1 adds to c (gradients of several

@@ -28,6 +28,8 @@ int make_gmm_plan(const moe_gmm *d, int64_t rows, GmmPlan *out) {
     if (!d || rows < 0 || rows > INT32_MAX - 1024) return MOE_ERR_INVALID_ARG;
     if (d->kind != MOE_GMM_NT && d->kind != MOE_GMM_NN && d->kind != MOE_GMM_TN) return MOE_ERR_INVALID_ARG;
     if (d->groups < 1 || d->groups > gmm::kMaxGroups || d->n < 1 || d->k < 1) return MOE_ERR_INVALID_ARG;
+    // the kernels' 32-bit places step past the last one by a few slices, like those of rows
+    if (d->n > INT32_MAX - 1024 || d->k > INT32_MAX - 1024) return MOE_ERR_UNSUPPORTED;
     if (!dtype_ok(d->dtype) || !dtype_ok(d->out_dtype)) return MOE_ERR_INVALID_ARG;
     if (d->dtype == MOE_F32 && d->out_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
     if (d->accumulate != 0 && d->accumulate != 1) return MOE_ERR_INVALID_ARG;

@@ -506,6 +506,15 @@ def test_grouped_mm_refuses_weights_beyond_64_bits():
             assert moe.moe_grouped_mm(d, None, None, None, None, 0, 0) == moe.MOE_ERR_UNSUPPORTED, (kind, n, s)
 
 
+def test_grouped_mm_refuses_lengths_at_the_end_of_32_bits():
+    """A contraction (or width) whose place after the last slice would pass 2^31."""
+    for kind in KINDS:
+        for dt, step in ((moe.MOE_BF16, 8), (moe.MOE_F32, 4)):
+            for n, k in ((2 ** 31 - step, 8), (8, 2 ** 31 - step), (8, 2 ** 31 - 1024)):
+                d = moe.make_gmm(kind, 1, n, k, dt, moe.MOE_F32, accumulate=kind == moe.MOE_GMM_TN)
+                assert moe.moe_grouped_mm(d, None, None, None, None, 0, 0) in BAD, (kind, dt, n, k)
+
+
 def test_grouped_mm_limits_weights_only():
     """The limit of 2^40 bytes is one on a group's weights: n rows of the other operands are not a thing."""
     for kind, n, k, kw in ((moe.MOE_GMM_NT, 2 ** 20, 64, {}), (moe.MOE_GMM_NN, 2 ** 20, 64, dict(ldc=2 ** 19)),
