@@ -163,6 +163,9 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// Rows of each of the tiles of a segment of len rows; unsigned, as the sum may pass 2^31.
+__device__ __forceinline__ int tile_rows(int len, int tiles) { return (int)((unsigned)(len + (unsigned)tiles - 1) / tiles); }
+
 struct Tile {
     int g, f0, r0, rows;        // first f and row of the result; valid rows
     int nh, nsub;               // N of one instruction, instructions side by side (kWide: up to two)
@@ -201,7 +204,7 @@ template <int KIND>
 __device__ __forceinline__ void order_groups(const int *s_off, int G, int unit, int *cum, int *ord) {
     auto rows = [&](int g) { return s_off[g + 1] - s_off[g]; };
     auto tiles = [&](int g) { return (rows(g) + unit - 1) / unit; };
-    auto weight = [&](int g) { return KIND == TN ? rows(g) : rows(g) == 0 ? 0 : (rows(g) + tiles(g) - 1) / tiles(g); };
+    auto weight = [&](int g) { return KIND == TN ? rows(g) : rows(g) == 0 ? 0 : tile_rows(rows(g), tiles(g)); };
     for (int g = threadIdx.x; g < G; g += kTcThreads) {
         int at = g;
         if (G <= kOrdered) {
@@ -260,7 +263,7 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const int *s_off, const
         const int tiles = s_cum[lo + 1] - s_cum[lo];
         const int r = i - s_cum[lo] * p.m_tiles;
         t.f0 = r / tiles * kM;
-        const int len = s_off[t.g + 1] - s_off[t.g], size = (len + tiles - 1) / tiles;
+        const int len = s_off[t.g + 1] - s_off[t.g], size = tile_rows(len, tiles);
         if (kWide && size > kN) t.nsub = 2;
         t.nh = ((size + t.nsub - 1) / t.nsub + 15) & ~15;
         const int at = r % tiles * t.nh * t.nsub;

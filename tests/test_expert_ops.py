@@ -455,6 +455,38 @@ def test_grouped_mm_places_past_32_bits():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dt,width", [(BF, 8), (F32, 4)])
+def test_grouped_mm_most_rows(dt, width):
+    """The largest number of rows, most of them in one segment.  Entries are -1, 0 and 1, so the results are exact."""
+    rows, part = 2 ** 31 - 1025, 1 << 26
+    a = torch.empty(rows, width, dtype=dt, device="cuda")
+    for lo in range(0, rows, part):
+        a[lo:lo + part].random_(0, 3, generator=gen(lo)).sub_(1)
+    off = torch.tensor([0, 3, 17, rows], dtype=torch.int32, device="cuda")
+    b = torch.empty(3, width, width, dtype=dt, device="cuda").random_(0, 3, generator=gen(16)).sub_(1)
+    c = torch.full((rows, width), float("nan"), dtype=dt, device="cuda")
+    code = moe.dtype_code(dt)
+    moe.check(moe.moe_grouped_mm(moe.make_gmm(moe.MOE_GMM_NT, 3, width, width, code, code), a, b, c, off, rows))
+    assert status_clear() == 0
+    for g, (lo, hi) in enumerate(((0, 3), (3, 17))):
+        assert torch.equal(c[lo:hi].double(), a[lo:hi].double() @ b[g].double().t())
+    for lo in range(17, rows, part):
+        x = a[lo:min(lo + part, rows)].float()
+        want = sum(x[:, i:i + 1] * b[2, :, i].float() for i in range(width))
+        assert torch.equal(c[lo:lo + part].float(), want)
+    del c
+    # weight gradients of 1024 segments
+    off = torch.linspace(0, rows, 1025, dtype=F64).round().to(torch.int32).cuda()
+    dw = torch.empty(1024, width, width, device="cuda")
+    moe.check(moe.moe_grouped_mm(moe.make_gmm(moe.MOE_GMM_TN, 1024, width, width, code, moe.MOE_F32), a, a, dw, off, rows))
+    assert status_clear() == 0
+    o = off.tolist()
+    for g in (0, 1, 512, 1022, 1023):
+        x = a[o[g]:o[g + 1]].double()
+        assert torch.equal(dw[g].double(), x.t() @ x)
+
+
+@pytest.mark.gpu
 def test_grouped_mm_ragged_segment_behind_long_ones():
     """A segment whose length is no multiple of 16 behind one whose tiles take more than a second in all: the wait for
     its last slice begins with the call and is longer than any bound on one tile's work (2.2e15 operations, 1.6 s
