@@ -124,7 +124,10 @@ int launch_gmm_tc(gmm::Params p, const DeviceInfo &dev, cudaStream_t s) {
             MOE_TRY(make_map_k(&mn.m[i], p.A, 1, p.rows, KIND == gmm::NT ? p.k : p.n, p.lda, gmm::box_rows(i)));
     }
     const int64_t F = KIND == gmm::NT ? p.n : p.k, live = std::min<int64_t>(p.G, p.rows);
-    // Tile shapes, by what the host knows (segments are on the device): the row tiles there are at least.
+    // Tile shapes, by the row tiles to be expected where every group has rows (segments are on the device; the host knows
+    // their number and sum only).  Rows that crowd on one group make fewer tiles: 256 of them on one of 32 groups, n 4096,
+    // k 1024, take pairs and 13.9 us, single CTAs 9.8 us; spread evenly, 54.6 us.  1500 on two of 8 groups 19.2 us, with
+    // the two alone (wide pairs) 18.8 us.
     //  pairs (256 x 256) where they fill the machine: 32 x 4096 x 7168 over 512 rows each 714 us, single CTAs (128 x 128)
     //    963 us; 6 x 1536 x 768 over 34 rows 9.7 us, single CTAs 7.5 us (twice as many SMs read);
     //  wide pairs (256 x 512) where segments have more than 256 rows: 675 us against 714 us; 300 rows 482 against 556

@@ -268,7 +268,8 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const int *s_off, const
         t.nh = ((size + t.nsub - 1) / t.nsub + 15) & ~15;
         const int at = r % tiles * t.nh * t.nsub;
         t.r0 = s_off[t.g] + at;
-        t.rows = min(t.nh * t.nsub, len - at);   // not positive for a last tile that the rounding left empty
+        // never empty: a tile has at most the unit of rows that the segment's number of tiles was taken with
+        t.rows = min(t.nh * t.nsub, len - at);
         t.c0 = 0;
         t.nc = KIND == NT ? p.k : p.n;
     }
@@ -381,7 +382,6 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
         for (int i = first; i < total && ok; i += step) {
             const Tile t = tile(i);
             if (KIND == TN && lane == 0) *s_at = i;
-            if (KIND != TN && t.rows <= 0) continue;
             const int f = t.f0 + (int)rank * 128;
             const int half = kPair ? t.nh / 2 : t.nh;   // N rows of an instruction that this CTA loads
             const int r = t.r0 + (int)rank * half;
@@ -448,7 +448,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
             bool ok = true;
             for (int i = first; i < total && ok; i += step) {
                 const Tile t = tile(i);
-                if (KIND == TN ? t.nc == 0 : t.rows <= 0) continue;
+                if (KIND == TN && t.nc == 0) continue;
                 const uint32_t idesc = kIdesc | (static_cast<uint32_t>(t.nh >> 3) << 17);
                 const int nkb = (t.nc + kSl - 1) / kSl;
                 const int run = kSums ? run_length<kF32>(nkb) : nkb;
@@ -548,7 +548,6 @@ __device__ __forceinline__ void tc_body(const CUtensorMap &tmM, const NMaps &tmN
         int local = 0;
         for (int i = first; i < total; i += step) {
             const Tile t = tile(i);
-            if (t.rows <= 0) continue;
             const int f = t.f0 + (int)rank * 128 + q * 32 + lane;
             const bool f_ok = f < (KIND == NT ? p.n : p.k);
             TO *out = static_cast<TO *>(p.C) + ((KIND == TN ? (int64_t)t.g * p.n : 0) + t.r0) * p.ldc;
