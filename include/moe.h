@@ -444,8 +444,8 @@ int moe_grouped_mm(const moe_gmm *d, const void *a, const void *b, void *c, cons
  *   q  [rows, C] uint8, scales [rows, (C / width) * ceil(width / group)] uint8,
  *   both contiguous.
  * Activations and derivatives are computed in fp32 and rounded once.  fp32 rows:
- * Phi and the sigmoid are off by a few 2^-23 of themselves, times 1 + v^2 for
- * v < 0 (rounding of the exponents).  bf16 rows take the special-function unit,
+ * Phi and the sigmoid are off by at most 2^-23 (0.75 v^2 + 8) of themselves
+ * (rounding of the exponents).  bf16 rows take the special-function unit,
  * which dw (fp32) inherits: Phi is off by at most 2^-21, and for v < 0 by at most
  * 2^-11.8 of itself; the sigmoid by 2^-20 + |v| 2^-23 of itself. */
 enum { MOE_CKPT_INT8 = 0, MOE_CKPT_E4M3 = 1 };

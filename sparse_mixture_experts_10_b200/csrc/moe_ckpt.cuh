@@ -160,18 +160,14 @@ __device__ __forceinline__ float amax_group(const uint32_t (&raw)[4], int lanes)
 }
 
 // Phi(v), the normal distribution function, with its density, and the sigmoid, in the accuracy of the row type, for
-// v < 0 relative to Phi itself: fp32 rows take erfcf, expf and a division.  bf16 rows (rounded to 2^-8 afterwards)
-// take the special-function unit: Phi(-|v|) = t (q1 + t (q2 + ... + t q6)) exp(-v^2 / 2), t = 1 / (1 + c |v|), whose
+// v < 0 relative to Phi itself: fp32 rows take normal_cdf, expf and a division.  bf16 rows (rounded to 2^-8 afterwards)
+// take the special-function unit, and for Phi fewer terms of the same form: Phi(-|v|) = t (q1 + t (q2 + ... + t q6)) exp(-v^2 / 2), t = 1 / (1 + c |v|), whose
 // exponential is the density's too.  c and q are a fit of Phi(-x) exp(x^2 / 2) for x from 0 to 13.5 (Phi(-13.2) is
 // 2^-130) that minimises the larger of error / 7.5e-8 and relative error / 2^-11: it is off by at most 3e-8 and by at
 // most 2^-12.3 of Phi; the rounding of t and of the exponential adds up to 4e-7 near 0.
 template <typename T>
 __device__ __forceinline__ float phi(float v, float *density) {
-    constexpr float kDensity0 = 0.39894228040143268f;   // 1 / sqrt(2 pi)
-    if (sizeof(T) == 4) {
-        if (density) *density = expf(-0.5f * v * v) * kDensity0;
-        return normal_cdf(v);
-    }
+    if (sizeof(T) == 4) return normal_cdf(v, density);
     const float t = rcp_approx(fmaf(fabsf(v), 0.287f, 1.0f));
     const float e = ex2_approx(v * v * -0.7213475204444817f);         // log2(e) / 2
     float q = fmaf(t, -0.0936281755566597f, 0.3131586015224457f);
@@ -180,7 +176,7 @@ __device__ __forceinline__ float phi(float v, float *density) {
     q = fmaf(t, q, 0.09363754838705063f);
     q = fmaf(t, q, 0.11627483367919922f);
     const float below = q * t * e;
-    if (density) *density = e * kDensity0;
+    if (density) *density = e * 0.39894228040143268f;                 // 1 / sqrt(2 pi)
     return v < 0.f ? below : 1.0f - below;
 }
 template <typename T>

@@ -317,9 +317,6 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-// The normal distribution function; 1 + erff would cancel for v < 0 (0 from -5.6 down).
-__device__ __forceinline__ float normal_cdf(float v) { return 0.5f * erfcf(v * -0.70710678118654752f); }
-
 // Special-function unit: 1/x and 2^x (hardware approximations, relative
 // error about 2^-22; subnormal results flush to zero).
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -331,6 +328,28 @@ __device__ __forceinline__ float ex2_approx(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+
+// The normal distribution function Phi in fp32, for v < 0 relative to itself (0.5 (1 + erff) cancels there, to 0 from
+// -5.6 down), and its density: Phi(-|v|) = P(t) exp(-v^2 / 2), t = 1 / (1 + 0.35 |v|), P of degree 9 fitted to the least
+// relative error for |v| up to 13.5 (2^-24.5; Phi(-13.2) is 2^-130).  Against 64 bits the relative error is at most
+// 2^-23 (0.75 v^2 + 7.5), of the roundings of the exponent, t and the sum; the root mean square of v Phi(v) for
+// values of about 1 is 4e-8, with erff 6e-8, with erfcf 8e-8.
+__device__ __forceinline__ float normal_cdf(float v, float *density = nullptr) {
+    const float t = rcp_approx(fmaf(fabsf(v), 0.35f, 1.0f));
+    const float e = ex2_approx(v * v * -0.7213475204444817f);   // log2(e) / 2
+    float q = fmaf(t, -0.027792975306510925f, 0.13693049550056458f);
+    q = fmaf(t, q, -0.23993749916553497f);
+    q = fmaf(t, q, 0.139257550239563f);
+    q = fmaf(t, q, -0.007547222077846527f);
+    q = fmaf(t, q, 0.09772725403308868f);
+    q = fmaf(t, q, 0.12231413275003433f);
+    q = fmaf(t, q, 0.13937656581401825f);
+    q = fmaf(t, q, 0.139674112200737f);
+    q = fmaf(t, q, -2.4189355372072896e-06f);
+    if (density) *density = e * 0.39894228040143268f;           // 1 / sqrt(2 pi)
+    const float below = q * e;
+    return v < 0.f ? below : 1.0f - below;
 }
 
 }  // namespace moe

@@ -746,10 +746,11 @@ def test_ckpt_backward_matches_differences(act):
 
 def cdf_err(v, dt):
     """Relative error of the computed Phi for v < 0, where a small value is no difference of large ones.
-    fp32: erfc's argument is off by 2^-23 of itself (constant and product) and x erfc'(x) / erfc(x) is below
-    v^2 + 1.5 |v| there, erfcf is off by at most 4 steps, the products by 2.  bf16: the fit's 2^-12.3, the
-    exponent's 2^-23 v^2 / 2 (v^2 of an 8-bit value is exact) and 2^-18 of the special-function unit and the sum:
-    below 1.1 2^-12 down to v = -13.2."""
+    fp32: the exponent v^2 / 2 is rounded three times (v^2, the constant, the product), 0.75 v^2 of 2^-23; 2^x is off by
+    2 of them, t by 1.5 and the polynomial by up to twice as much for it, by 2 for its sum and fit, the product by 0.5:
+    0.75 v^2 + 7.5, below v^2 + 1.5 |v| + 6 from 1 on.  bf16: the fit's 2^-12.3, the exponent's 2^-23 v^2 / 2
+    (v^2 of an 8-bit value is exact) and 2^-18 of the special-function unit and the sum: below 1.1 2^-12 down to
+    v = -13.2."""
     return 2.0 ** -23 * (v * v + 1.5 * v.abs() + 6) if dt == F32 else torch.full_like(v, 1.1 * 2.0 ** -12)
 
 
@@ -778,8 +779,8 @@ def test_ckpt_gelu_of_negative_values_keeps_its_relative_error(dt):
     assert status_clear() == 0
     wt, below = w.to(F64)[:, None], cdf(v)
     close(hw, wt * v * below, wt * (v * below).abs() * (cdf_err(v, dt) + 2.0 ** -23))
-    slope = v * torch.exp(-0.5 * v * v) / math.sqrt(2 * math.pi)   # v times the density, off by 2^-23 (v^2 / 2 + 8)
-    close(du, wt * (below + slope), wt * (below * cdf_err(v, dt) + slope.abs() * 2.0 ** -23 * (v * v / 2 + 8) +
+    slope = v * torch.exp(-0.5 * v * v) / math.sqrt(2 * math.pi)   # v times the density, off by 2^-23 (0.75 v^2 + 8)
+    close(du, wt * (below + slope), wt * (below * cdf_err(v, dt) + slope.abs() * 2.0 ** -23 * (0.75 * v * v + 8) +
                                         (below + slope).abs() * 2.0 ** -23))
 
 
