@@ -1187,6 +1187,35 @@ def test_q4_quantize_and_dequantize(fmt, group, dt):
         close(out, values, torch.zeros_like(torch.nan_to_num(values)))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [moe.MOE_Q4_INT4, moe.MOE_Q4_E2M1])
+def test_q4_places_past_32_bits(fmt):
+    """The last expert of a tensor whose codes (and weights) pass 2^32: as if it stood alone."""
+    N, n, k = 66, 16384, 8192
+    W = torch.zeros(N, n, k, dtype=BF, device="cuda")
+    W[-1] = randn(gen(51), n, k, std=0.05)
+    codes = torch.full((N, n, k // 2), 0x5A, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(N, n, k // 32, dtype=BF if fmt == moe.MOE_Q4_INT4 else torch.uint8, device="cuda")
+    alone = [torch.empty_like(t[:1]) for t in (codes, scales, W)]
+    big, one = moe.make_q4(N, n, k, 32, fmt), moe.make_q4(1, n, k, 32, fmt)
+    moe.check(moe.moe_q4_quantize(big, W, moe.MOE_BF16, codes, scales))
+    moe.check(moe.moe_q4_quantize(one, W[-1:].contiguous(), moe.MOE_BF16, alone[0], alone[1]))
+    assert torch.equal(codes[-1:], alone[0]) and torch.equal(scales[-1:], alone[1])
+    W.fill_(1.0)
+    moe.check(moe.moe_q4_dequantize(big, codes, scales, W, moe.MOE_BF16))
+    moe.check(moe.moe_q4_dequantize(one, alone[0], alone[1], alone[2], moe.MOE_BF16))
+    assert torch.equal(W[-1:], alone[2]) and int((W[:-1] != 0).sum()) == 0
+    x = randn(gen(52), 1, k)
+    y, y1 = torch.empty(1, n, device="cuda"), torch.empty(1, n, device="cuda")
+    for d, c, s, e, out in ((big, codes, scales, N - 1, y), (one, alone[0], alone[1], 0, y1)):
+        ex = torch.tensor([e], dtype=torch.int32, device="cuda")
+        moe.check(moe.moe_q4_matvec(d, x, 1, 1, ex, c, s, None, out, moe.MOE_F32))
+    assert status_clear() == 0
+    assert torch.equal(y, y1)
+    w = q4_values(alone[0][0, -64:], alone[1][0, -64:], k, 32, fmt)
+    close(y[0, -64:], w @ x[0].to(F64), (k + 8) * 2.0 ** -23 * (w.abs() @ x[0].to(F64).abs()))
+
+
 def test_q4_refusals():
     ok = dict(experts=4, n=32, k=64, group=32)
 
