@@ -16,8 +16,11 @@
 // and 270 us, two: 210 and 261 us, four: 208 and 251 us forward and backward
 // for 65536 rows of 2 x 2048 bf16, that is 5.2 and 5.4 TB/s); the group's
 // maximum is a shuffle tree over the 4 to 32 lanes that hold it.  GELU and e4m3 in
-// 12289 rows of 2200: 35 and 45 us, 3.8 and 4.2 TB/s (the activation's
-// instructions).
+// 12289 rows of 2200: 36 and 45 us, 3.8 and 4.2 TB/s (the activation's
+// instructions); in fp32 54 and 72 us, 4.5 and 4.9 TB/s.  SwiGLU and int8 in 32768
+// rows of 2 x 2048 fp32: 190 and 240 us, 4.9 and 5.0 TB/s.  Reading back, one piece a
+// lane: 65536 rows of 2 x 2048 bf16 in 188 us, 4.3 TB/s (two thirds of it writes);
+// 32768 in fp32 in 151 us, 4.4 TB/s.
 #pragma once
 
 #include <cuda_fp8.h>

@@ -32,7 +32,8 @@
 // to each, whatever the tile's shape; a slice of a 256 x 512 tile is 48 KB a CTA
 // for 17 MFLOP, of a 256 x 256 one 32 KB for 8) beside the power cap; few rows, HBM.
 // 32 experts of 512 rows each, n 4096, k 7168: 675 us, 1425 TFLOP/s with 256 x 512
-// tiles, 714 us with 256 x 256, 963 us with single CTAs.  Weight gradients over
+// tiles, 714 us with 256 x 256, 963 us with single CTAs; of 512 +- 20 rows each 753 us
+// in bf16, 815 us in fp32.  Weight gradients over
 // 512 rows (18 of 4096 x 2048, fp32): 171 us, 3.5 TB/s written.
 //
 // Every wait is bounded; on expiry the waiting role stops issuing work, the
