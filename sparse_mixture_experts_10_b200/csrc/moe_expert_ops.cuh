@@ -474,8 +474,9 @@ int moe_q4_matvec(const moe_q4 *d, const void *x, int64_t pairs, int32_t x_div, 
     q4::MatvecParams p{};
     MOE_TRY(make_q4_params(d, &p));
     if (pairs < 0 || x_div < 1 || !dtype_ok(y_dtype)) return MOE_ERR_INVALID_ARG;
-    if (pairs > q4::kMaxPairs || q4::matvec_smem(3, 1, p.k, pairs) > q4::kRoom) return MOE_ERR_UNSUPPORTED;
+    if (pairs > q4::kMaxPairs) return MOE_ERR_UNSUPPORTED;
     if (pairs == 0) return MOE_OK;
+    if (q4::matvec_smem(3, 1, p.k, pairs) > q4::kRoom) return MOE_ERR_UNSUPPORTED;
     if (!x || !expert || !codes || !scales || !y) return MOE_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) || !aligned16(y) || !aligned4(expert) || !aligned4(gate))
         return MOE_ERR_INVALID_ARG;

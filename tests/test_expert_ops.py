@@ -1089,6 +1089,8 @@ def test_q4_matvec_refuses_rows_beyond_shared_memory():
             d = moe.make_q4(4, 32, k, 32, fmt)
             rc = moe.moe_q4_matvec(d, 256, pairs, 1, 256, 256, 256, None, 256, moe.MOE_F32, 0)
             assert rc == moe.MOE_ERR_UNSUPPORTED, (k, pairs, rc)
+    # no pairs: nothing to do, whatever the rows
+    assert moe.moe_q4_matvec(moe.make_q4(4, 32, 1 << 20, 32), None, 0, 1, None, None, None, None, None, 0, 0) == moe.MOE_OK
 
 
 @pytest.mark.gpu
